@@ -19,6 +19,7 @@ import torch
 
 __all__ = ["forward", "step", "forward_workspace_bytes", "step_workspace_bytes", "plan_info",
            "forward_blocks", "forward_blocks_workspace_bytes", "temporal_conv",
+           "rotary_tables", "qk_norm_rope", "qk_norm_rope_backward",
            "shard_begin", "shard_end", "shard_workspace_bytes", "device_status", "selftest_bounded_wait",
            "LclaError", "LIB_PATH", "lib", "BF16", "F32", "D", "HEAD_DIMS"]
 
@@ -57,6 +58,16 @@ def _load() -> ctypes.CDLL:
     L.lcla_forward_blocks.restype = I
     L.lcla_temporal_conv.argtypes = [P, I, I, I, I, P, P, P, I, P, I, P]
     L.lcla_temporal_conv.restype = I
+    LL, DB = ctypes.c_longlong, ctypes.c_double
+    L.lcla_rotary_tables.argtypes = [P, LL, I, I, P, P, DB, I, DB, DB, DB, DB, P, P, P]
+    L.lcla_rotary_tables.restype = I
+    L.lcla_qk_norm_rope.argtypes = [P, LL, P, LL, I, I, I, I, I, P, P, F, P, P, I, I, I, P, P, LL, P, LL, I, P]
+    L.lcla_qk_norm_rope.restype = I
+    L.lcla_qk_norm_rope_backward_workspace_bytes.argtypes = [I]
+    L.lcla_qk_norm_rope_backward_workspace_bytes.restype = Z
+    L.lcla_qk_norm_rope_backward.argtypes = [P, LL, P, LL, P, LL, P, LL, I, I, I, I, I, P, P, F, P, P, I, I, I, P,
+                                             P, LL, P, LL, P, P, I, P, Z, P]
+    L.lcla_qk_norm_rope_backward.restype = I
     L.lcla_shard_workspace_bytes.argtypes = [I, I, I, I, I, I]
     L.lcla_shard_workspace_bytes.restype = Z
     L.lcla_shard_begin.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, Z, P]
@@ -335,3 +346,173 @@ def temporal_conv(x: torch.Tensor, tokens_per_frame: int, weight: torch.Tensor,
     _check(lib.lcla_temporal_conv(_ptr(x), B, N // S, S, C, _ptr(weight), _ptr(bias), _ptr(cache),
                                   int(bool(save)), _ptr(out), code, _stream(stream, x.device)))
     return out
+
+
+class _on:
+    """Makes a tensor's device the current one while the library launches on it."""
+
+    def __init__(self, device: torch.device):
+        self._to, self._was = device.index, torch.cuda.current_device()
+
+    def __enter__(self):
+        if self._to != self._was:
+            torch.cuda.set_device(self._to)
+
+    def __exit__(self, *exc):
+        if self._to != self._was:
+            torch.cuda.set_device(self._was)
+
+
+def _array(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, device) -> None:
+    """A contiguous CUDA tensor of this shape, dtype and device, or None."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Optional[torch.Tensor] = None,
+                  theta: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: float = 4096,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda",
+                  out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``lcla_rotary_tables``: (cos, sin) [n, sum(dims) / 2] fp32 of n tokens.
+
+    ``dims`` holds the rotary dims of each axis (an int for one axis).  Tokens
+    stand at ``positions`` [axes, n] ([n] for one axis) int64, or at indices
+    ``first`` .. ``first + n - 1`` of a row-major grid whose inner axes have
+    the sizes ``extents``.  ``scaling``: "none", "linear", "ntk" or "yarn"."""
+    dims = [int(x) for x in ([dims] if isinstance(dims, int) else dims)]
+    extents = None if extents is None else [int(x) for x in extents]
+    n = int(n)
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    if not 1 <= len(dims) <= 3:
+        raise ValueError("one to three axes")
+    if n < 0 or min(dims) < 0:
+        raise ValueError("negative sizes")
+    if positions is None and len(dims) > 1 and (extents is None or len(extents) != len(dims) - 1):
+        raise ValueError("extents must hold the sizes of the inner axes")
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
+            raise TypeError("positions must be a CUDA tensor")
+        device = positions.device
+        _array("positions", positions, (n,) if positions.dim() == 1 and len(dims) == 1 else (len(dims), n), torch.int64,
+               device)
+    elif out is not None:
+        device = out[0].device
+    else:
+        device = torch.device(device)
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+    shape = (n, sum(dims) // 2)
+    cos, sin = out if out is not None else (torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2))
+    _array("cos", cos, shape, torch.float32, device)
+    _array("sin", sin, shape, torch.float32, device)
+    ints = ctypes.c_int * 3
+    with _on(device):
+        _check(lib.lcla_rotary_tables(_ptr(positions), int(first), n, len(dims), ints(*dims),
+                                      None if extents is None else ints(*extents), float(theta),
+                                      ROPE_SCALING[scaling], float(factor), float(original_len), float(beta_fast),
+                                      float(beta_slow), _ptr(cos), _ptr(sin), _stream(stream, device)))
+    return cos, sin
+
+
+def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> int:
+    """The distance between the tokens of ``t`` [B, N, H, d], in elements: heads
+    lie side by side, tokens at one distance throughout."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, H, d]")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the shape, dtype and device of its forward tensor")
+    B, N, H, d = t.shape
+    if t.numel() == 0:
+        return H * d
+    if t.stride(3) != 1 and d > 1 or t.stride(2) != d and H > 1:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if N > 1:
+        if B > 1 and t.stride(0) != N * t.stride(1):
+            raise ValueError(f"{name}: tokens must be evenly spaced over the batch")
+        return t.stride(1)
+    return t.stride(0) if B > 1 else H * d
+
+
+def _norm_inputs(q, k, cos, sin, q_weight, k_weight, positions):
+    ldq = _rows("q", q)
+    B, N, H, d = q.shape
+    code = _dtype_code(q)
+    Hk, ldk = 0, 0
+    if k is not None:
+        ldk = _rows("k", k)
+        if k.shape[:2] != q.shape[:2] or k.shape[3] != d or k.dtype != q.dtype or k.device != q.device:
+            raise ValueError("k must be [B, N, Hk, d] of q's dtype on q's device")
+        Hk = k.shape[2]
+    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+        raise ValueError("rope tables must be [rows, rotary_dims / 2]")
+    for name, t in (("cos", cos), ("sin", sin)):
+        _array(name, t, cos.shape, torch.float32, q.device)
+    _array("q_weight", q_weight, (d,), torch.float32, q.device)
+    _array("k_weight", k_weight, (d,), torch.float32, q.device)
+    _array("positions", positions, (B, N), torch.int64, q.device)
+    return B, N, H, Hk, d, code, ldq, ldk
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], rope_cos: torch.Tensor, rope_sin: torch.Tensor, *,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 positions: Optional[torch.Tensor] = None, half_layout: bool = False,
+                 out: Optional[Tuple[torch.Tensor, Optional[torch.Tensor]]] = None,
+                 stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``lcla_qk_norm_rope``: RMS norm of every head of q [B, N, H, d] and k
+    [B, N, Hk, d] (or None), with weights [d], then the rotation of the first
+    2 * rope_cos.shape[1] entries by the table rows at ``positions`` [B, N]
+    int64 (token n's own row without).  q and k may be column windows of one
+    projection; ``out`` = (q_out, k_out) may be (q, k) themselves."""
+    B, N, H, Hk, d, code, ldq, ldk = _norm_inputs(q, k, rope_cos, rope_sin, q_weight, k_weight, positions)
+    if out is None:
+        out = (torch.empty((B, N, H, d), dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty((B, N, Hk, d), dtype=q.dtype, device=q.device))
+    qo, ko = out
+    with _on(q.device):
+        _check(lib.lcla_qk_norm_rope(
+            _ptr(q), ldq, _ptr(k), ldk, B, N, H, Hk, d, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope_cos),
+            _ptr(rope_sin), rope_cos.shape[0], 2 * rope_cos.shape[1], int(bool(half_layout)), _ptr(positions),
+            _ptr(qo), _rows("out q", qo, q), _ptr(ko), 0 if k is None else _rows("out k", ko, k), code,
+            _stream(stream, q.device)))
+    return qo, ko
+
+
+def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
+                          k: Optional[torch.Tensor], rope_cos: torch.Tensor, rope_sin: torch.Tensor, *,
+                          q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                          eps: float = 1e-6, positions: Optional[torch.Tensor] = None, half_layout: bool = False,
+                          out: Optional[Tuple[torch.Tensor, Optional[torch.Tensor]]] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """``lcla_qk_norm_rope_backward``: (dq, dk, dq_weight, dk_weight) from the
+    gradients of ``qk_norm_rope``'s outputs and its inputs; a weight that was
+    not given has no gradient (None)."""
+    B, N, H, Hk, d, code, ldq, ldk = _norm_inputs(q, k, rope_cos, rope_sin, q_weight, k_weight, positions)
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight without k")
+    if out is None:
+        out = (torch.empty((B, N, H, d), dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty((B, N, Hk, d), dtype=q.dtype, device=q.device))
+    dq, dk = out
+    dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
+    need = int(lib.lcla_qk_norm_rope_backward_workspace_bytes(d))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    with _on(q.device):
+        _check(lib.lcla_qk_norm_rope_backward(
+            _ptr(dq_out), _rows("dq_out", dq_out, q), _ptr(dk_out), 0 if k is None else _rows("dk_out", dk_out, k),
+            _ptr(q), ldq, _ptr(k), ldk, B, N, H, Hk, d, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope_cos),
+            _ptr(rope_sin), rope_cos.shape[0], 2 * rope_cos.shape[1], int(bool(half_layout)), _ptr(positions),
+            _ptr(dq), _rows("out q", dq, q), _ptr(dk), 0 if k is None else _rows("out k", dk, k), _ptr(dqw), _ptr(dkw),
+            code, _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, q.device)))
+    return dq, dk, dqw, dkw

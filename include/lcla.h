@@ -278,6 +278,101 @@ LCLA_API int lcla_step(const void *q_blk, const void *k_blk, const void *v_blk,
               void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Rotary tables, made on the device: the rope_cos / rope_sin arrays that every
+ * other entry point reads ("Implementing Block Causal Linear Attention ...",
+ * section "Rotary Position Embeddings": one frequency set per axis of the
+ * latent).  With P = sum of axis_dims / 2, entry p of axis a, pair j of D =
+ * axis_dims[a]:
+ *   cos[n][p] = amp cos(pos_a(n) f),  sin[n][p] = amp sin(pos_a(n) f),
+ *   f = theta^(-2j/D), then by `scaling` for contexts `factor` times longer:
+ *     LCLA_ROPE_LINEAR  f / factor (position interpolation);
+ *     LCLA_ROPE_NTK     theta replaced by theta factor^(D/(D-2)) (D >= 4);
+ *     LCLA_ROPE_YARN    f (g + (1-g) / factor), g = clamp((original_len f /
+ *                       2 pi - beta_slow) / (beta_fast - beta_slow), 0, 1),
+ *                       and amp = 0.1 ln(factor) + 1 (Peng et al., "YaRN:
+ *                       Efficient Context Window Extension of Large Language
+ *                       Models", the NTK-by-parts ramp and the temperature).
+ *                       amp = 1 otherwise.
+ *   positions     [axes][N] int64 device, 8-byte aligned, or NULL: token n then
+ *                 stands at index first + n of a row-major grid, pos_a =
+ *                 (index / product of the extents after a) mod extent of a
+ *                 (the first axis is not wrapped).  Angles are reduced exactly,
+ *                 so far positions lose nothing; each entry is within 2e-7 of
+ *                 amp times its cosine or sine.
+ *   axis_dims     HOST array of `axes` (1..3) even sizes, sum <= 256.
+ *   axis_extents  HOST array of axes - 1 extents of the inner axes (e.g. rows
+ *                 and columns of a latent frame); NULL when axes = 1 or
+ *                 positions are given.
+ *   theta >= 1; factor >= 1 (read unless LCLA_ROPE_NONE); original_len > 0 and
+ *   beta_fast > beta_slow >= 0 (read for LCLA_ROPE_YARN); 0 <= first <= 2^60.
+ *   rope_cos/sin  [N, P] float32 device.  Written.
+ * Returns an lcla_status (N = 0: LCLA_OK, nothing enqueued).
+ */
+typedef enum {
+    LCLA_ROPE_NONE = 0,
+    LCLA_ROPE_LINEAR = 1,
+    LCLA_ROPE_NTK = 2,
+    LCLA_ROPE_YARN = 3
+} lcla_rope_scaling;
+
+LCLA_API int lcla_rotary_tables(const long long *positions, long long first, int N, int axes,
+                 const int *axis_dims, const int *axis_extents, double theta, int scaling,
+                 double factor, double original_len, double beta_fast, double beta_slow,
+                 float *rope_cos, float *rope_sin, void *stream);
+
+/*
+ * RMS norm of each head's query and key, and the rotation, in one pass.  A row
+ * x is one head of one token, d entries:
+ *   n = x rsqrt(mean(x^2) + eps) w,
+ *   y = n with its first rotary_dims entries turned: pairs (2p, 2p+1), or
+ *       (p, p + rotary_dims / 2) when half_layout = 1, by (x, y) -> (x c - y s,
+ *       x s + y c), c, s = row positions[b][n] (row n without positions), column
+ *       p of the tables.  A position outside the tables takes their first or
+ *       last row.
+ *   q, k          token t = b N + n, head h at element t ldq + h d (t ldk + h
+ *                 d), so they may be column windows of a fused projection;
+ *                 H >= 1 and Hk >= 0 heads (Hk = 0: the k arrays may be NULL).
+ *   q_out, k_out  the same form; each may be its own input (the same pointer
+ *                 and ld), and must not otherwise overlap anything.
+ *   d             a multiple of 8, <= 256.  0 <= rotary_dims <= d, even; a
+ *                 multiple of 16 with half_layout = 1.
+ *   q_weight, k_weight  [d] float32 device, or NULL (ones).
+ *   rope_cos/sin  [table_rows, rotary_dims / 2] float32 device; table_rows >= N
+ *                 without positions.  May be NULL when rotary_dims = 0.
+ *   positions     [B, N] int64 device, 8-byte aligned, or NULL.
+ * Pointers 16-byte aligned, lds a multiple of 16 bytes and at least the width
+ * of the heads.  Computed in fp32, rounded once.  An all-zero row with eps = 0
+ * gives NaN, as the formula does.  Returns an lcla_status.
+ */
+LCLA_API int lcla_qk_norm_rope(const void *q, long long ldq, const void *k, long long ldk,
+                 int B, int N, int H, int Hk, int d,
+                 const float *q_weight, const float *k_weight, float eps,
+                 const float *rope_cos, const float *rope_sin, int table_rows, int rotary_dims,
+                 int half_layout, const long long *positions,
+                 void *q_out, long long ldq_out, void *k_out, long long ldk_out,
+                 int dtype, void *stream);
+
+/*
+ * Its gradient: from dq_out, dk_out (the gradients of q_out, k_out) and the
+ * forward's inputs, dq and dk in the same form, and the weights' gradients
+ * summed over all tokens and heads in a fixed order ([d] float32 each, or NULL;
+ * only where that weight was given).  dq may be dq_out itself and dk dk_out.
+ * The workspace is needed when a weight's gradient is: at least
+ * lcla_qk_norm_rope_backward_workspace_bytes(d) bytes, 16-byte aligned.
+ */
+LCLA_API size_t lcla_qk_norm_rope_backward_workspace_bytes(int d);
+LCLA_API int lcla_qk_norm_rope_backward(const void *dq_out, long long lddq_out,
+                 const void *dk_out, long long lddk_out,
+                 const void *q, long long ldq, const void *k, long long ldk,
+                 int B, int N, int H, int Hk, int d,
+                 const float *q_weight, const float *k_weight, float eps,
+                 const float *rope_cos, const float *rope_sin, int table_rows, int rotary_dims,
+                 int half_layout, const long long *positions,
+                 void *dq, long long lddq, void *dk, long long lddk,
+                 float *dq_weight, float *dk_weight, int dtype,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * How lcla_forward cuts this problem, for benchmarks and tests: writes
  * info[0] = 1 when tiles hold whole blocks (d = 32 and block_len < 64), else 0;
  * info[1] = segments (partial states written by the first pass);
