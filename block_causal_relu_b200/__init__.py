@@ -20,6 +20,7 @@ import torch
 __all__ = ["forward", "step", "forward_workspace_bytes", "step_workspace_bytes", "plan_info",
            "forward_blocks", "forward_blocks_workspace_bytes", "temporal_conv",
            "rotary_tables", "qk_norm_rope", "qk_norm_rope_backward",
+           "gated_forward", "gated_step", "gated_backward",
            "shard_begin", "shard_end", "shard_workspace_bytes", "device_status", "selftest_bounded_wait",
            "LclaError", "LIB_PATH", "lib", "BF16", "F32", "D", "HEAD_DIMS"]
 
@@ -68,6 +69,14 @@ def _load() -> ctypes.CDLL:
     L.lcla_qk_norm_rope_backward.argtypes = [P, LL, P, LL, P, LL, P, LL, I, I, I, I, I, P, P, F, P, P, I, I, I, P,
                                              P, LL, P, LL, P, P, I, P, Z, P]
     L.lcla_qk_norm_rope_backward.restype = I
+    for f in (L.lcla_gated_forward_workspace_bytes, L.lcla_gated_backward_workspace_bytes):
+        f.argtypes, f.restype = [I, I, I, I, I], Z
+    L.lcla_gated_forward.argtypes = [P, P, P, P, I, I, I, I, F, P, P, P, I, P, Z, P]
+    L.lcla_gated_forward.restype = I
+    L.lcla_gated_step.argtypes = [P, P, P, P, I, I, I, I, F, P, I, P, I, P, Z, P]
+    L.lcla_gated_step.restype = I
+    L.lcla_gated_backward.argtypes = [P, P, P, P, P, I, I, I, I, F, P, P, P, P, P, P, P, I, P, Z, P]
+    L.lcla_gated_backward.restype = I
     L.lcla_shard_workspace_bytes.argtypes = [I, I, I, I, I, I]
     L.lcla_shard_workspace_bytes.restype = Z
     L.lcla_shard_begin.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, Z, P]
@@ -516,3 +525,111 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
             _ptr(dq), _rows("out q", dq, q), _ptr(dk), 0 if k is None else _rows("out k", dk, k), _ptr(dqw), _ptr(dkw),
             code, _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, q.device)))
     return dq, dk, dqw, dkw
+
+
+def _gated_inputs(q, k, v, g, scale):
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+    if q.dim() != 4:
+        raise ValueError("q, k, v must share one [B, N, H, d] shape")
+    code = _dtype_code(q)
+    _array("q", q, q.shape, q.dtype, q.device)
+    _array("k", k, q.shape, q.dtype, q.device)
+    _array("v", v, q.shape, q.dtype, q.device)
+    B, N, H, d = q.shape
+    if g is None:
+        raise TypeError("g must be a CUDA tensor")
+    _array("g", g, (B, N, H), torch.float32, q.device)
+    return B, N, H, d, code, float(d ** -0.5 if scale is None else scale)
+
+
+def _workspace(workspace, need: int, device):
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def gated_forward_workspace_bytes(B: int, H: int, N: int, d: int, dtype: int) -> int:
+    return int(lib.lcla_gated_forward_workspace_bytes(B, H, N, d, dtype))
+
+
+def gated_backward_workspace_bytes(B: int, H: int, N: int, d: int, dtype: int) -> int:
+    return int(lib.lcla_gated_backward_workspace_bytes(B, H, N, d, dtype))
+
+
+def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, scale: Optional[float] = None, *,
+                  state_in: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  state_out: Optional[torch.Tensor] = None, want_state: bool = True,
+                  workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``lcla_gated_forward``: S_t = exp(g_t) S_{t-1} + v_t k_t^T, out_t =
+    scale S_t q_t over q, k, v [B, N, H, d] with log decays g [B, N, H] fp32 and
+    scale d^-1/2 unless given.  Returns (out, state after the last token
+    [B, H, d, d] fp32 or None)."""
+    B, N, H, d, code, scale = _gated_inputs(q, k, v, g, scale)
+    st = (B, H, d, d)
+    _array("state_in", state_in, st, torch.float32, q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    if state_out is None and want_state:
+        state_out = torch.empty(st, dtype=torch.float32, device=q.device)
+    _array("out", out, q.shape, q.dtype, q.device)
+    _array("state_out", state_out, st, torch.float32, q.device)
+    workspace, size = _workspace(workspace, gated_forward_workspace_bytes(B, H, N, d, code), q.device)
+    with _on(q.device):
+        _check(lib.lcla_gated_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), B, H, N, d, scale, _ptr(state_in), _ptr(out),
+                                      _ptr(state_out), code, _ptr(workspace), size, _stream(stream, q.device)))
+    return out, state_out
+
+
+def gated_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor, save: bool,
+               scale: Optional[float] = None, *, state_out: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """``lcla_gated_step``: one block [B, L, H, d] (one token, when serving)
+    against ``state`` [B, H, d, d] fp32.  With ``save`` the state after the block
+    goes to ``state_out``, or to ``state`` itself.  Returns the block's outputs."""
+    if state is None:
+        raise TypeError("state must be a CUDA tensor")
+    if state_out is not None:
+        return gated_forward(q, k, v, g, scale, state_in=state, out=out, state_out=state_out if save else None,
+                             want_state=False, workspace=workspace, stream=stream)[0]
+    B, L, H, d, code, scale = _gated_inputs(q, k, v, g, scale)
+    _array("state", state, (B, H, d, d), torch.float32, q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    _array("out", out, q.shape, q.dtype, q.device)
+    workspace, size = _workspace(workspace, gated_forward_workspace_bytes(B, H, L, d, code), q.device)
+    with _on(q.device):
+        _check(lib.lcla_gated_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), B, H, L, d, scale, _ptr(state), int(bool(save)),
+                                   _ptr(out), code, _ptr(workspace), size, _stream(stream, q.device)))
+    return out
+
+
+def gated_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                   scale: Optional[float] = None, *, state_in: Optional[torch.Tensor] = None,
+                   dstate_out: Optional[torch.Tensor] = None, want_dstate_in: bool = False,
+                   out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """``lcla_gated_backward``: (dq, dk, dv, dg, dstate_in or None) from the
+    gradients of ``gated_forward``'s outputs and its inputs; ``out`` gives the
+    buffers of the first four."""
+    B, N, H, d, code, scale = _gated_inputs(q, k, v, g, scale)
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a CUDA tensor")
+    _array("dout", dout, q.shape, q.dtype, q.device)
+    st = (B, H, d, d)
+    _array("state_in", state_in, st, torch.float32, q.device)
+    _array("dstate_out", dstate_out, st, torch.float32, q.device)
+    dq, dk, dv, dg = out if out is not None else (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q),
+                                                 torch.empty_like(g))
+    for name, t, like in (("dq", dq, q), ("dk", dk, q), ("dv", dv, q), ("dg", dg, g)):
+        _array(name, t, like.shape, like.dtype, q.device)
+    ds = torch.empty(st, dtype=torch.float32, device=q.device) if want_dstate_in else None
+    workspace, size = _workspace(workspace, gated_backward_workspace_bytes(B, H, N, d, code), q.device)
+    with _on(q.device):
+        _check(lib.lcla_gated_backward(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(g), B, H, N, d, scale,
+                                       _ptr(state_in), _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+                                       _ptr(ds), code, _ptr(workspace), size, _stream(stream, q.device)))
+    return dq, dk, dv, dg, ds

@@ -1,0 +1,696 @@
+// lcla_gated.cuh -- device code of the gated recurrence (lcla_gated_* in
+// include/lcla.h).
+//
+// Per (batch entry, head), with a fp32 state S [value][key]:
+//   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t.
+// In tiles of 32 tokens, G the running sum of g inside the tile (inclusive),
+// G_C its last value, S0 the state before the tile:
+//   o_t / scale = e^{G_t} S0 q_t + sum_{s <= t} e^{G_t - G_s} (q_t . k_s) v_s
+//   S1          = e^{G_C} S0 + sum_s (e^{G_C - G_s} v_s) k_s^T
+// With R_t the gradient of the loss by S_t divided by scale, R_t = e^{g_{t+1}}
+// R_{t+1} + do_t q_t^T, the gradients are the same sums:
+//   dq = scale S_t^T do_t   the recurrence with (query, key, value) = (do, v, k);
+//   dk = scale R_t^T v_t    the reversed one with (v, do, q);
+//   dv = scale R_t k_t      the reversed one with (k, q, do).
+// The reversed recurrence runs through the tiles from the last one, with
+//   o_s / scale = e^{G_C - G_s} R q_s + sum_{t >= s} e^{G_t - G_s} (q_s . k_t) v_t
+//   R           <- e^{G_C} R + sum_t (e^{G_t} v_t) k_t^T.
+//
+// All exponents are differences of G taken in one tile.  G is summed in double
+// and kept as a whole part and a fraction in fp32, so that a difference is
+// exact to 2^-24 however strong the decays of the tokens before it are.
+//
+// One warp owns 32 rows (values) of one head's state in registers, as the
+// accumulator of 16x8 matrix instructions, and walks the tiles of a segment
+// alone; at head dim 64 the two warps of a head share the tiles.  The layout of
+// an accumulator is also that of an operand, so neither the state nor the
+// weighted scores pass through shared memory.
+#ifndef LCLA_GATED_CUH
+#define LCLA_GATED_CUH
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lcla {
+namespace gated {
+
+constexpr int TILE = 32;           // tokens per tile
+constexpr int WARPS = 4;           // warps per block: 4 heads at d = 32, 2 at d = 64
+constexpr int THREADS = WARPS * 32;
+constexpr float RESET = -1000.f;   // a log decay below this counts as this: e^-1000 is zero in fp32
+
+// ---------------------------------------------------------------- operands
+// A pair is two neighbouring entries of the contraction index in one lane.  In<T> holds them as given: one bf16x2
+// register, or the two tf32 terms of each float.  Co<T, NT> holds computed fp32 values: NT bf16 terms (8 bits each, so
+// 3 terms keep all 24 bits of an fp32 value and 2 keep 16), or two tf32 terms (22 bits).
+template <typename T>
+struct In;
+template <>
+struct In<__nv_bfloat16> {
+    uint32_t u;
+};
+template <>
+struct In<float> {
+    uint32_t h[2], l[2];
+};
+template <typename T, int NT>
+struct Co {
+    uint32_t u[NT];
+};
+template <int NT>
+struct Co<float, NT> {
+    uint32_t h[2], l[2];
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t tf32(float x)
+{
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int NT>
+__device__ __forceinline__ void split(Co<__nv_bfloat16, NT> &o, float x, float y)
+{
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        o.u[i] = pack_bf16(x, y);
+        if (i + 1 < NT) {
+            x -= lo_f(o.u[i]);
+            y -= hi_f(o.u[i]);
+        }
+    }
+}
+template <typename P>
+__device__ __forceinline__ void split_tf32(P &o, float x, float y)
+{
+    o.h[0] = tf32(x);
+    o.h[1] = tf32(y);
+    o.l[0] = tf32(x - __uint_as_float(o.h[0]));
+    o.l[1] = tf32(y - __uint_as_float(o.h[1]));
+}
+template <int NT>
+__device__ __forceinline__ void split(Co<float, NT> &o, float x, float y)
+{
+    split_tf32(o, x, y);
+}
+__device__ __forceinline__ float2 value(const In<__nv_bfloat16> &p) { return make_float2(lo_f(p.u), hi_f(p.u)); }
+__device__ __forceinline__ float2 value(const In<float> &p)
+{
+    return make_float2(__uint_as_float(p.h[0]) + __uint_as_float(p.l[0]),
+                       __uint_as_float(p.h[1]) + __uint_as_float(p.l[1]));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// c += A B over 16 entries of the contraction.  A's pairs: (row l/4, k 0-7), (row l/4 + 8, k 0-7), (row l/4, k 8-15),
+// (row l/4 + 8, k 8-15); B's: (k 0-7), (k 8-15) of column l/4.  The smallest products are added first.
+__device__ __forceinline__ void mma(float (&c)[4], const In<__nv_bfloat16> (&a)[4], const In<__nv_bfloat16> &b0,
+                                    const In<__nv_bfloat16> &b1)
+{
+    mma_bf16(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u, b1.u);
+}
+template <int NT>
+__device__ __forceinline__ void mma(float (&c)[4], const Co<__nv_bfloat16, NT> (&a)[4], const In<__nv_bfloat16> &b0,
+                                    const In<__nv_bfloat16> &b1)
+{
+#pragma unroll
+    for (int i = NT - 1; i >= 0; --i) mma_bf16(c, a[0].u[i], a[1].u[i], a[2].u[i], a[3].u[i], b0.u, b1.u);
+}
+template <int NT>
+__device__ __forceinline__ void mma(float (&c)[4], const In<__nv_bfloat16> (&a)[4], const Co<__nv_bfloat16, NT> &b0,
+                                    const Co<__nv_bfloat16, NT> &b1)
+{
+#pragma unroll
+    for (int i = NT - 1; i >= 0; --i) mma_bf16(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u[i], b1.u[i]);
+}
+template <typename PA, typename PB>
+__device__ __forceinline__ void mma_split(float (&c)[4], const PA (&a)[4], const PB &b0, const PB &b1)
+{
+    // a tf32 instruction contracts 8 entries: slots 0-3 take the first of each pair, slots 4-7 the second
+    mma_tf32(c, a[0].l[0], a[1].l[0], a[0].l[1], a[1].l[1], b0.h[0], b0.h[1]);
+    mma_tf32(c, a[2].l[0], a[3].l[0], a[2].l[1], a[3].l[1], b1.h[0], b1.h[1]);
+    mma_tf32(c, a[0].h[0], a[1].h[0], a[0].h[1], a[1].h[1], b0.l[0], b0.l[1]);
+    mma_tf32(c, a[2].h[0], a[3].h[0], a[2].h[1], a[3].h[1], b1.l[0], b1.l[1]);
+    mma_tf32(c, a[0].h[0], a[1].h[0], a[0].h[1], a[1].h[1], b0.h[0], b0.h[1]);
+    mma_tf32(c, a[2].h[0], a[3].h[0], a[2].h[1], a[3].h[1], b1.h[0], b1.h[1]);
+}
+__device__ __forceinline__ void mma(float (&c)[4], const In<float> (&a)[4], const In<float> &b0, const In<float> &b1)
+{
+    mma_split(c, a, b0, b1);
+}
+template <int NT>
+__device__ __forceinline__ void mma(float (&c)[4], const Co<float, NT> (&a)[4], const In<float> &b0,
+                                    const In<float> &b1)
+{
+    mma_split(c, a, b0, b1);
+}
+template <int NT>
+__device__ __forceinline__ void mma(float (&c)[4], const In<float> (&a)[4], const Co<float, NT> &b0,
+                                    const Co<float, NT> &b1)
+{
+    mma_split(c, a, b0, b1);
+}
+
+// -------------------------------------------------------- tiles in shared memory
+// A tile holds 32 token rows of one head, d entries each.  16-byte pieces are swapped inside a row by the row's number,
+// so that the 8 rows that a matrix load touches fall on different banks.
+template <typename T, int D>
+struct Tile {
+    static constexpr int RB = D * (int)sizeof(T);   // bytes of a row: 64, 128 or 256
+    static constexpr int BYTES = TILE * RB;
+    static constexpr int PIECES = RB / 16;
+
+    __device__ static __forceinline__ uint32_t at(int row, int piece)
+    {
+        const int key = RB == 64 ? (row >> 1) & 3 : row & 7;
+        return row * RB + ((piece ^ key) << 4);
+    }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ float lds(uint32_t addr)
+{
+    float r;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ float2 lds2(uint32_t addr)
+{
+    float2 r;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t lds_u(uint32_t addr)
+{
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+
+// A operand: rows 16 m + [0, 16) of the tile, entries 16 ks + [0, 16).
+template <int D>
+__device__ __forceinline__ void load_a(In<__nv_bfloat16> (&a)[4], uint32_t tile, int m, int ks, int lane)
+{
+    const int row = 16 * m + (lane & 15), piece = 2 * ks + (lane >> 4);
+    ldsm4(tile + Tile<__nv_bfloat16, D>::at(row, piece), a[0].u, a[1].u, a[2].u, a[3].u);
+}
+template <int D>
+__device__ __forceinline__ void load_a(In<float> (&a)[4], uint32_t tile, int m, int ks, int lane)
+{
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int row = 16 * m + (lane >> 2) + 8 * (p & 1), col = 16 * ks + 8 * (p >> 1) + 2 * (lane & 3);
+        const float2 v = lds2(tile + Tile<float, D>::at(row, col >> 2) + 4 * (col & 3));
+        split_tf32(a[p], v.x, v.y);
+    }
+}
+// B operands of two column tiles: columns are the rows 16 sb + [0, 16) of the tile, contraction over 16 ks + [0, 16).
+template <int D>
+__device__ __forceinline__ void load_b(In<__nv_bfloat16> (&b)[2][2], uint32_t tile, int sb, int ks, int lane)
+{
+    const int row = 16 * sb + (lane & 7) + 8 * (lane >> 4), piece = 2 * ks + ((lane >> 3) & 1);
+    ldsm4(tile + Tile<__nv_bfloat16, D>::at(row, piece), b[0][0].u, b[0][1].u, b[1][0].u, b[1][1].u);
+}
+template <int D>
+__device__ __forceinline__ void load_b(In<float> (&b)[2][2], uint32_t tile, int sb, int ks, int lane)
+{
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int row = 16 * sb + 8 * n + (lane >> 2), col = 16 * ks + 8 * p + 2 * (lane & 3);
+            const float2 v = lds2(tile + Tile<float, D>::at(row, col >> 2) + 4 * (col & 3));
+            split_tf32(b[n][p], v.x, v.y);
+        }
+}
+// Transposed: contraction over the rows 16 sb + [0, 16), entries 16 fb + [0, 16) as columns; t[fh][kh] holds entry
+// 16 fb + 8 fh + l/4 of the rows 16 sb + 8 kh + 2 (l%4) + {0, 1}.
+template <int D>
+__device__ __forceinline__ void load_t(In<__nv_bfloat16> (&t)[2][2], uint32_t tile, int sb, int fb, int lane)
+{
+    const int row = 16 * sb + (lane & 15), piece = 2 * fb + (lane >> 4);
+    ldsm4t(tile + Tile<__nv_bfloat16, D>::at(row, piece), t[0][0].u, t[0][1].u, t[1][0].u, t[1][1].u);
+}
+template <int D>
+__device__ __forceinline__ void load_t(In<float> (&t)[2][2], uint32_t tile, int sb, int fb, int lane)
+{
+#pragma unroll
+    for (int fh = 0; fh < 2; ++fh)
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+            const int row = 16 * sb + 8 * kh + 2 * (lane & 3), col = 16 * fb + 8 * fh + (lane >> 2);
+            const float x = lds(tile + Tile<float, D>::at(row, col >> 2) + 4 * (col & 3));
+            const float y = lds(tile + Tile<float, D>::at(row + 1, col >> 2) + 4 * (col & 3));
+            split_tf32(t[fh][kh], x, y);
+        }
+}
+
+// ------------------------------------------------------------------ work
+// One recurrence of a launch: the forward, or one of the gradient's three.
+struct Role {
+    const void *q, *k, *v;   // query, key, value [B, N, H, d]
+    const void *x;           // dot: the tensor whose rows meet the output's, or NULL
+    void *out;
+    float *dot;              // [d / 32][B, H, N]: sign * <x, out> over each 32 entries
+    const float *state;      // state before each segment [nseg][B, H, d, d], or of the whole call (nseg = 1), or NULL (zero)
+    float *state_end;        // nseg = 1: the state after the last token, or NULL
+    float sign;
+};
+
+struct Work {
+    const float *g;          // [B, N, H]
+    int B, H, N, nseg, seg_tiles;   // segments of seg_tiles tiles
+    float scale;
+};
+
+// Weights of a tile, per warp, in shared memory.
+struct Weights {
+    float2 split[TILE];      // whole part and fraction of G / ln 2 (negated in the reversed recurrence)
+    float in[TILE];          // weight of the carried state in each token's output
+    float out[TILE];         // weight of each token in the next state
+};
+
+// Reads one log decay per lane; returns the decay of the whole tile and, in `total`, its G / ln 2.
+template <bool REV>
+__device__ __forceinline__ float tile_weights(Weights *w, float g, int lane, double &total)
+{
+    double G = (double)(g < RESET ? RESET : g) * 1.4426950408889634;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, G, o);
+        if (lane >= o) G += up;
+    }
+    const double end = __shfl_sync(0xffffffffu, G, 31);
+    const double whole = floor(G);
+    const float a = (float)whole, b = (float)(G - whole);
+    const float fromstart = ex2((float)G), toend = ex2((float)(end - G));
+    __syncwarp();                          // the previous tile's weights have been read
+    w->split[lane] = REV ? make_float2(-a, -b) : make_float2(a, b);
+    w->in[lane] = REV ? toend : fromstart;
+    w->out[lane] = REV ? fromstart : toend;
+    __syncwarp();
+    total = end;
+    return ex2((float)end);
+}
+
+template <int NS>
+__device__ __forceinline__ void group_sync(int group)
+{
+    if (NS == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * NS) : "memory");
+}
+
+// The NS warps of a head copy 32 token rows of it into a tile; rows past N are filled with zeros.
+template <typename T, int D>
+__device__ __forceinline__ void copy_tile(uint32_t tile, const char *base, size_t row_bytes, int t0, int N, int tid)
+{
+    using L = Tile<T, D>;
+    constexpr int NT = D;                                  // threads of a head: 32 per 32 entries
+    constexpr int RPI = NT / L::PIECES;                    // rows per step
+    const int piece = tid % L::PIECES, r0 = tid / L::PIECES;
+    const char *p = base + (size_t)(t0 + r0) * row_bytes + piece * 16;
+#pragma unroll
+    for (int r = 0; r < TILE; r += RPI, p += RPI * row_bytes) {
+        const bool live = t0 + r0 + r < N;
+        const uint32_t dst = tile + L::at(r0 + r, piece);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(live ? p : base),
+                     "r"(live ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// S <- decay S + sum over the tile's tokens of (weight v) k^T, for the warp's 32 values and all keys.  Each tile's
+// sum starts from zero and meets the state in one rounded multiply-add: the matrix units cut off low bits as they
+// accumulate, which a long sum in them would collect.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, uint32_t vt, const Weights *w, int slab,
+                                       float decay, int lane)
+{
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        Co<T, NT> a[2][4];
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb) {
+            In<T> v[2][2];
+            load_t<D>(v, vt, sb, 2 * slab + m, lane);
+#pragma unroll
+            for (int kh = 0; kh < 2; ++kh) {
+                const float2 u = *reinterpret_cast<const float2 *>(&w->out[16 * sb + 8 * kh + 2 * (lane & 3)]);
+#pragma unroll
+                for (int fh = 0; fh < 2; ++fh) {
+                    const float2 x = value(v[fh][kh]);
+                    split(a[sb][2 * kh + fh], x.x * u.x, x.y * u.y);
+                }
+            }
+        }
+#pragma unroll
+        for (int eb = 0; eb < D / 16; ++eb) {
+            In<T> k[2][2][2];
+            load_t<D>(k[0], kt, 0, eb, lane);
+            load_t<D>(k[1], kt, 1, eb, lane);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                mma(c, a[0], k[0][n][0], k[0][n][1]);
+                mma(c, a[1], k[1][n][0], k[1][n][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[m][2 * eb + n][i] = fmaf(S[m][2 * eb + n][i], decay, c[i]);
+            }
+        }
+    }
+}
+
+// The warp's rows of a [d][d] state in global memory; TR: the state lies transposed ([key][value]).
+template <int D, bool TR>
+__device__ __forceinline__ void read_state(float (&S)[2][D / 8][4], const float *p, int slab, int lane)
+{
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = 32 * slab + 16 * m + 8 * h + (lane >> 2), e = 8 * n + 2 * (lane & 3);
+                float2 v = make_float2(0.f, 0.f);
+                if (p) {
+                    if (TR) v = make_float2(p[e * D + c], p[(e + 1) * D + c]);
+                    else v = *reinterpret_cast<const float2 *>(p + c * D + e);
+                }
+                S[m][n][2 * h] = v.x;
+                S[m][n][2 * h + 1] = v.y;
+            }
+}
+template <int D>
+__device__ __forceinline__ void write_state(const float (&S)[2][D / 8][4], float *p, int slab, int lane)
+{
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = 32 * slab + 16 * m + 8 * h + (lane >> 2), e = 8 * n + 2 * (lane & 3);
+                *reinterpret_cast<float2 *>(p + c * D + e) = make_float2(S[m][n][2 * h], S[m][n][2 * h + 1]);
+            }
+}
+
+template <typename T>
+__device__ __forceinline__ void write_rows(T *out, size_t row, const float (&acc)[4][4], int t, int N, int lane);
+
+// Two rows (t, t + 8) of 32 outputs.  A lane holds two neighbouring entries of each of four 8-entry tiles; fp32 stores
+// them as they are (a quad fills 32 bytes).
+template <>
+__device__ __forceinline__ void write_rows<float>(float *out, size_t row, const float (&acc)[4][4], int t, int N,
+                                                  int lane)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (t + 8 * h < N)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                *reinterpret_cast<float2 *>(out + (size_t)(8 * h) * row + 8 * n + 2 * (lane & 3)) =
+                    make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+}
+// bf16: neighbouring lanes swap one register, so that each stores 8 bytes and a quad fills 32.
+template <>
+__device__ __forceinline__ void write_rows<__nv_bfloat16>(__nv_bfloat16 *out, size_t row, const float (&acc)[4][4],
+                                                          int t, int N, int lane)
+{
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < 4; n += 2) {
+            const uint32_t a = pack_bf16(acc[n][2 * h], acc[n][2 * h + 1]);
+            const uint32_t b = pack_bf16(acc[n + 1][2 * h], acc[n + 1][2 * h + 1]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            // even lanes keep tile n, odd lanes tile n + 1
+            const uint2 v = odd ? make_uint2(got, b) : make_uint2(a, got);
+            if (t + 8 * h < N)
+                *reinterpret_cast<uint2 *>(out + (size_t)(8 * h) * row + 8 * (n + odd) + 4 * ((lane & 3) >> 1)) = v;
+        }
+}
+
+// One recurrence over one segment of one head.  NP, NS_, NU: bf16 terms of the weighted scores, of the state where it
+// meets the query, and of the weighted values of an update.
+template <typename T, int D, bool REV, bool TR, bool DOT, int NP, int NQ, int NU, int STAGES>
+__device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h, int seg, int group, int slab, int lane,
+                                      uint32_t ring, Weights *wt)
+{
+    using L = Tile<T, D>;
+    constexpr int NS = D / 32, TENSORS = DOT ? 4 : 3, STAGE = TENSORS * L::BYTES;
+    const int tiles = (w.N + TILE - 1) / TILE;
+    const int first = seg * w.seg_tiles, n = min(w.seg_tiles, tiles - first);
+    if (n <= 0) return;
+    const size_t row = (size_t)w.H * D, row_bytes = row * sizeof(T);
+    const size_t at = (size_t)b * w.N * row + (size_t)h * D;
+    const char *src[4] = {(const char *)((const T *)r.q + at), (const char *)((const T *)r.k + at),
+                          (const char *)((const T *)r.v + at), DOT ? (const char *)((const T *)r.x + at) : nullptr};
+    const float *gp = w.g + (size_t)b * w.N * w.H + h;
+    T *out = (T *)r.out + at + 32 * slab;
+    const int tid = slab * 32 + lane;
+    auto tile_at = [&](int i) { return (REV ? first + n - 1 - i : first + i) * TILE; };
+    auto load = [&](int i) {
+        if (i < n) {
+            const uint32_t s = ring + (i % STAGES) * STAGE;
+#pragma unroll
+            for (int j = 0; j < TENSORS; ++j) copy_tile<T, D>(s + j * L::BYTES, src[j], row_bytes, tile_at(i), w.N, tid);
+        }
+        commit();
+    };
+    auto load_g = [&](int i) {
+        const int t = i < n ? tile_at(i) + lane : w.N;
+        return t < w.N ? gp[(size_t)t * w.H] : 0.f;
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) load(i);
+    float g = load_g(0);
+
+    float S[2][D / 8][4];
+    const float *st = r.state;
+    if (st) st += (((size_t)(w.nseg > 1 ? seg : 0) * w.B + b) * w.H + h) * D * D;
+    read_state<D, TR>(S, st, slab, lane);
+
+    for (int i = 0; i < n; ++i) {
+        const float gnext = load_g(i + 1);
+        double total;
+        const float decay = tile_weights<REV>(wt, g, lane, total);
+        g = gnext;
+        wait_copies<STAGES - 2>();
+        group_sync<NS>(group);               // this tile has landed for every warp, and the last one's slot is free
+        load(i + STAGES - 1);
+        const uint32_t qt = ring + (i % STAGES) * STAGE, kt = qt + L::BYTES, vt = kt + L::BYTES, xt = vt + L::BYTES;
+        const int t0 = tile_at(i);
+
+        // the carried state's part of the outputs
+        float acc[2][4][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            In<T> a[2][4];
+            load_a<D>(a[0], qt, 0, ks, lane);
+            load_a<D>(a[1], qt, 1, ks, lane);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                Co<T, NQ> s0, s1;
+                split(s0, S[c >> 1][2 * ks][2 * (c & 1)], S[c >> 1][2 * ks][2 * (c & 1) + 1]);
+                split(s1, S[c >> 1][2 * ks + 1][2 * (c & 1)], S[c >> 1][2 * ks + 1][2 * (c & 1) + 1]);
+                mma(acc[0][c], a[0], s0, s1);
+                mma(acc[1][c], a[1], s0, s1);
+            }
+        }
+        // the tile's own part, 16 queries at a time
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float2 gq[2];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int t = 16 * m + 8 * hh + (lane >> 2);
+                gq[hh] = wt->split[t];
+                const float wi = wt->in[t];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    acc[m][c][2 * hh] *= wi;
+                    acc[m][c][2 * hh + 1] *= wi;
+                }
+            }
+#pragma unroll
+            for (int sb = REV ? m : 0; sb <= (REV ? 1 : m); ++sb) {
+                float sc[2][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    In<T> a[4], k[2][2];
+                    load_a<D>(a, qt, m, ks, lane);
+                    load_b<D>(k, kt, sb, ks, lane);
+                    mma(sc[0], a, k[0][0], k[0][1]);
+                    mma(sc[1], a, k[1][0], k[1][1]);
+                }
+                Co<T, NP> p[4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int s = 16 * sb + 8 * nt + 2 * (lane & 3);
+                    const float4 gk = *reinterpret_cast<const float4 *>(&wt->split[s]);
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int t = 16 * m + 8 * hh + (lane >> 2);
+                        float x = sc[nt][2 * hh] * ex2((gq[hh].x - gk.x) + (gq[hh].y - gk.y));
+                        float y = sc[nt][2 * hh + 1] * ex2((gq[hh].x - gk.z) + (gq[hh].y - gk.w));
+                        if (sb == m) {
+                            x = (REV ? s >= t : s <= t) ? x : 0.f;
+                            y = (REV ? s + 1 >= t : s + 1 <= t) ? y : 0.f;
+                        }
+                        split(p[2 * nt + hh], x, y);
+                    }
+                }
+#pragma unroll
+                for (int cb = 0; cb < 2; ++cb) {
+                    In<T> v[2][2];
+                    load_t<D>(v, vt, sb, 2 * slab + cb, lane);
+                    mma(acc[m][2 * cb], p, v[0][0], v[0][1]);
+                    mma(acc[m][2 * cb + 1], p, v[1][0], v[1][1]);
+                }
+            }
+            const int t = t0 + 16 * m + (lane >> 2);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][c][j] *= w.scale;
+            if (DOT) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    float s = 0.f;
+                    const int rr = 16 * m + 8 * hh + (lane >> 2);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = 32 * slab + 8 * c + 2 * (lane & 3);
+                        float2 x;
+                        if (sizeof(T) == 4) {
+                            x = lds2(xt + L::at(rr, col >> 2) + 4 * (col & 3));
+                        } else {
+                            const uint32_t u = lds_u(xt + L::at(rr, col >> 3) + 2 * (col & 7));
+                            x = make_float2(lo_f(u), hi_f(u));
+                        }
+                        s = fmaf(x.x, acc[m][c][2 * hh], s);
+                        s = fmaf(x.y, acc[m][c][2 * hh + 1], s);
+                    }
+                    s += __shfl_xor_sync(0xffffffffu, s, 1);
+                    s += __shfl_xor_sync(0xffffffffu, s, 2);
+                    if ((lane & 3) == 0 && t + 8 * hh < w.N)
+                        r.dot[(((size_t)slab * w.B + b) * w.H + h) * w.N + t + 8 * hh] = r.sign * s;
+                }
+            }
+            write_rows<T>(out + (size_t)t * row, row, acc[m], t, w.N, lane);
+        }
+        update<T, D, NU>(S, kt, vt, wt, slab, decay, lane);
+    }
+    wait_copies<0>();
+    if (r.state_end) write_state<D>(S, r.state_end + ((size_t)b * w.H + h) * D * D, slab, lane);
+}
+
+// What a segment adds to the state, from zero, and its decay.
+template <typename T, int D, bool REV, int STAGES>
+__device__ __forceinline__ void total(const Work &w, const void *key, const void *val, float *part, float *decays, int b,
+                                      int h, int seg, int group, int slab, int lane, uint32_t ring, Weights *wt)
+{
+    using L = Tile<T, D>;
+    constexpr int NS = D / 32, STAGE = 2 * L::BYTES;
+    const int tiles = (w.N + TILE - 1) / TILE;
+    const int first = seg * w.seg_tiles, n = min(w.seg_tiles, tiles - first);
+    const size_t row = (size_t)w.H * D, row_bytes = row * sizeof(T);
+    const size_t at = (size_t)b * w.N * row + (size_t)h * D;
+    const char *kp = (const char *)((const T *)key + at), *vp = (const char *)((const T *)val + at);
+    const float *gp = w.g + (size_t)b * w.N * w.H + h;
+    const int tid = slab * 32 + lane;
+    auto tile_at = [&](int i) { return (REV ? first + n - 1 - i : first + i) * TILE; };
+    auto load = [&](int i) {
+        if (i < n) {
+            const uint32_t s = ring + (i % STAGES) * STAGE;
+            copy_tile<T, D>(s, kp, row_bytes, tile_at(i), w.N, tid);
+            copy_tile<T, D>(s + L::BYTES, vp, row_bytes, tile_at(i), w.N, tid);
+        }
+        commit();
+    };
+    auto load_g = [&](int i) {
+        const int t = i < n ? tile_at(i) + lane : w.N;
+        return t < w.N ? gp[(size_t)t * w.H] : 0.f;
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) load(i);
+    float g = load_g(0);
+    float S[2][D / 8][4] = {};
+    double sum = 0.0;
+    for (int i = 0; i < n; ++i) {
+        const float gnext = load_g(i + 1);
+        double t;
+        const float decay = tile_weights<REV>(wt, g, lane, t);
+        sum += t;
+        g = gnext;
+        wait_copies<STAGES - 2>();
+        group_sync<NS>(group);
+        load(i + STAGES - 1);
+        const uint32_t kt = ring + (i % STAGES) * STAGE;
+        update<T, D, 3>(S, kt, kt + L::BYTES, wt, slab, decay, lane);
+    }
+    wait_copies<0>();
+    const size_t at_s = ((size_t)seg * w.B + b) * w.H + h;
+    write_state<D>(S, part + at_s * D * D, slab, lane);
+    if (decays && slab == 0 && lane == 0) decays[at_s] = ex2((float)sum);
+}
+
+}  // namespace gated
+}  // namespace lcla
+
+#endif

@@ -373,6 +373,64 @@ LCLA_API int lcla_qk_norm_rope_backward(const void *dq_out, long long lddq_out,
                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Gated linear recurrence: linear attention over a state that decays, with one
+ * log decay per token and head.  For each batch entry and head, S [value]
+ * [key] in fp32,
+ *   S_t = e^{g_t} S_{t-1} + v_t k_t^T,    out_t = scale S_t q_t,
+ * S before the first token being state_in (zero when NULL).  No feature map,
+ * rotation or normaliser is applied (lcla_qk_norm_rope prepares q and k).
+ *   q, k, v, out  [B, N, H, d] device, dtype; d = 32 or 64.
+ *   g             [B, N, H] float32 device, 4-byte aligned (so is dg): log
+ *                 decays, normally <= 0.  A value
+ *                 below -1000, -infinity included, counts as -1000: its e^g is
+ *                 zero, which starts a new sequence inside a packed one.
+ *   state_in, state_out  [B, H, d, d] float32 device, each may be NULL;
+ *                 state_out may be state_in itself.  N = 0 copies the state.
+ *   scale         1e-18 <= |scale| <= 1e18.
+ *   workspace     lcla_gated_forward_workspace_bytes(...) bytes, 16-byte
+ *                 aligned (NULL when 0); not shared with a call in flight.
+ * Everything else must not overlap.  q, k, v and the states must be finite: a
+ * NaN or infinity of one token can also reach the outputs of the up to 31
+ * tokens before it that share its tile.  bf16 scores and states enter the
+ * matrix units as sums of two to three bf16 terms, fp32 ones as two tf32 terms,
+ * so that outputs are fp32 results rounded once.  Returns an lcla_status.
+ */
+LCLA_API size_t lcla_gated_forward_workspace_bytes(int B, int H, int N, int d, int dtype);
+LCLA_API int lcla_gated_forward(const void *q, const void *k, const void *v, const float *g,
+                 int B, int H, int N, int d, float scale, const float *state_in,
+                 void *out, float *state_out, int dtype,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same for a block of L tokens (one, when serving) against a carried
+ * state, as lcla_step: out uses state and the block; save != 0 leaves the state
+ * after the block in `state`, save = 0 leaves it bit-unchanged.  Workspace as
+ * lcla_gated_forward with N = L (none for L <= 16).
+ */
+LCLA_API int lcla_gated_step(const void *q, const void *k, const void *v, const float *g,
+                 int B, int H, int L, int d, float scale, float *state, int save,
+                 void *out, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of lcla_gated_forward from dout (of out) and dstate_out (of
+ * state_out; NULL: zero), given the forward's inputs; nothing of the forward is
+ * kept between the calls.  With R_t = e^{g_{t+1}} R_{t+1} + scale dout_t q_t^T
+ * and R past the last token = dstate_out:
+ *   dq_t = scale S_t^T dout_t,  dk_t = R_t^T v_t,  dv_t = R_t k_t,
+ *   dg_t = e^{g_t} <S_{t-1}, R_t> (0 where g_t is below -1000),
+ *   dstate_in = e^{g_0} R_0.
+ *   dq, dk, dv    [B, N, H, d] device, dtype.  dg [B, N, H] float32 device.
+ *   dstate_in     [B, H, d, d] float32 device, or NULL; may be dstate_out.
+ * Same rules as the forward; sums run in a fixed order.
+ */
+LCLA_API size_t lcla_gated_backward_workspace_bytes(int B, int H, int N, int d, int dtype);
+LCLA_API int lcla_gated_backward(const void *dout, const void *q, const void *k, const void *v,
+                 const float *g, int B, int H, int N, int d, float scale,
+                 const float *state_in, const float *dstate_out,
+                 void *dq, void *dk, void *dv, float *dg, float *dstate_in, int dtype,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * How lcla_forward cuts this problem, for benchmarks and tests: writes
  * info[0] = 1 when tiles hold whole blocks (d = 32 and block_len < 64), else 0;
  * info[1] = segments (partial states written by the first pass);
