@@ -66,42 +66,59 @@ __device__ __forceinline__ Weights *weights_of()
     return reinterpret_cast<Weights *>(smem + S::G * S::RING) + (threadIdx.x >> 5);
 }
 
+// Blocks of a kernel on an SM, which bounds its registers, and tiles in flight per head.
 template <typename T, int D>
-struct Ring {   // tiles in flight per head: what keeps three blocks (two of fp32 at d = 64) on an SM
-    static constexpr int MAIN = sizeof(T) * D >= 256 ? 2 : 3;
-    static constexpr int TOTAL = sizeof(T) * D >= 256 ? 3 : 4;
+struct Shape {
+    static constexpr int BLOCKS = sizeof(T) == 2 ? (D == 32 ? 3 : 2) : 2;
+    static constexpr int STAGES = sizeof(T) == 2 && D == 64 ? 3 : 2;
+    static constexpr int QK_STAGES = 2;
+    static constexpr int TOTAL_BLOCKS = BLOCKS;
+    static constexpr int TOTAL_STAGES = STAGES + 1;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(THREADS, 3) gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
+// NU: terms of a state update.  Where the state after the call comes out of the scan, the state in here only meets
+// bf16 outputs and two terms keep it exact enough for them; where it is itself an output, three do.
+template <typename T, int D, int NU>
+__global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
+gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
 {
-    using S = Smem<T, D, 3, Ring<T, D>::MAIN>;
+    constexpr int ST = Shape<T, D>::STAGES;
+    using S = Smem<T, D, 3, ST>;
     const Place p = place<D>(w.H, 1);
     if (!p.live) return;
-    recur<T, D, false, false, false, 2, 2, 3, Ring<T, D>::MAIN>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane,
-                                                               ring_of<S>(p), weights_of<S>());
+    recur<T, D, FORWARD, false, 2, 2, NU, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
+                                                   weights_of<S>());
 }
 
+// dq and dk side by side: the same instructions for both directions, since two unrolled bodies together overflow the
+// instruction cache (measured at d = 64: warps waited for instructions 2.3 of 6 cycles with three bodies in a launch).
+// Their outputs also give dg, which is fp32: every factor keeps three terms.
 struct Roles {
-    Role r[3];
+    Role r[2];
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS, 3) gated_backward_k(const __grid_constant__ Work w, const __grid_constant__ Roles rs)
+__global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
+gated_backward_qk_k(const __grid_constant__ Work w, const __grid_constant__ Roles rs)
 {
-    constexpr int ST = Ring<T, D>::MAIN;
+    constexpr int ST = Shape<T, D>::QK_STAGES;
     using S = Smem<T, D, 4, ST>;
-    const Place p = place<D>(w.H, 3);
+    const Place p = place<D>(w.H, 2);
     if (!p.live) return;
-    if (p.role == 0)
-        recur<T, D, false, true, true, 3, 3, 3, ST>(w, rs.r[0], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                                    weights_of<S>());
-    else if (p.role == 1)
-        recur<T, D, true, true, true, 3, 3, 3, ST>(w, rs.r[1], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                                   weights_of<S>());
-    else
-        recur<T, D, true, false, false, 2, 2, 2, ST>(w, rs.r[2], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                                     weights_of<S>());
+    recur<T, D, EITHER, true, 3, 3, 3, ST>(w, rs.r[p.role], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
+                                           weights_of<S>());
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
+gated_backward_v_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
+{
+    constexpr int ST = Shape<T, D>::STAGES;
+    using S = Smem<T, D, 3, ST>;
+    const Place p = place<D>(w.H, 1);
+    if (!p.live) return;
+    recur<T, D, REVERSED, false, 2, 2, 2, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
+                                              weights_of<S>());
 }
 
 struct Totals {
@@ -110,19 +127,15 @@ struct Totals {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS, 3) gated_totals_k(const __grid_constant__ Work w, const __grid_constant__ Totals t,
-                                                             int roles)
+__global__ void __launch_bounds__(THREADS, (Shape<T, D>::TOTAL_BLOCKS))
+gated_totals_k(const __grid_constant__ Work w, const __grid_constant__ Totals t, int roles)
 {
-    constexpr int ST = Ring<T, D>::TOTAL;
+    constexpr int ST = Shape<T, D>::TOTAL_STAGES;
     using S = Smem<T, D, 2, ST>;
     const Place p = place<D>(w.H, roles);
     if (!p.live) return;
-    if (p.role == 0)
-        total<T, D, false, ST>(w, t.key[0], t.val[0], t.part[0], t.decays, p.b, p.h, p.seg, p.group, p.slab, p.lane,
-                               ring_of<S>(p), weights_of<S>());
-    else
-        total<T, D, true, ST>(w, t.key[1], t.val[1], t.part[1], nullptr, p.b, p.h, p.seg, p.group, p.slab, p.lane,
-                              ring_of<S>(p), weights_of<S>());
+    total<T, D, 3, ST>(w, t.key[p.role], t.val[p.role], t.part[p.role], p.role ? nullptr : t.decays, p.role == 1, p.b,
+                       p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p), weights_of<S>());
 }
 
 struct Scan {
@@ -191,42 +204,60 @@ struct GradGate {
 
 // dg_t = <S, R> at the segment's end + the sum over the segment's tokens from t on of <q, dq> - <k, dk>.  The sum over
 // all later tokens would be the same number, as a difference of two long sums that nearly cancel; starting again at
-// each segment's end keeps it to 32-bit accuracy.  One warp per segment of a head.
-__global__ void __launch_bounds__(128) gated_dgate_k(const __grid_constant__ GradGate p)
+// each segment's end keeps it to 32-bit accuracy.  One block per segment of a head (at most 32 tiles): each warp takes
+// every fourth tile, latest first, reads all of them at once and sums each from its end.
+constexpr int kGateTiles = 32;     // tiles of a segment at most
+__global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__ GradGate p)
 {
-    const int lane = threadIdx.x & 31;
-    const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int BH = p.B * p.H;
-    if (u >= (long long)BH * p.nseg) return;
-    const int bh = (int)(u % BH), seg = (int)(u / BH), b = bh / p.H, h = bh % p.H;
+    constexpr int PER = kGateTiles / WARPS;
+    __shared__ float sums[kGateTiles + WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = p.B * p.H;
+    const int bh = (int)(blockIdx.x % (unsigned)BH), seg = (int)(blockIdx.x / (unsigned)BH), b = bh / p.H, h = bh % p.H;
     const int t0 = seg * p.seg_tiles * TILE, t1 = min(p.N, t0 + p.seg_tiles * TILE);
-    if (t0 >= t1) return;
+    const size_t plane = (size_t)BH * p.N;
+    const float *dot = p.dot + (size_t)bh * p.N;
+    float d[PER], g[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int t = t1 - 1 - lane - 32 * (warp + WARPS * i);    // lane 0 has the latest token
+        d[i] = g[i] = 0.f;
+        if (t >= t0) {
+            d[i] = dot[t];
+            for (int k = 1; k < p.planes; ++k) d[i] += dot[k * plane + t];
+            g[i] = p.g[((size_t)b * p.N + t) * p.H + h];
+        }
+    }
     const float4 *S = reinterpret_cast<const float4 *>(p.before) + ((size_t)(seg + 1) * BH + bh) * p.n4;
     const float4 *R = reinterpret_cast<const float4 *>(p.after) + ((size_t)seg * BH + bh) * p.n4;
     float y = 0.f;
-    for (int i = lane; i < p.n4; i += 32) {
+    for (int i = threadIdx.x; i < p.n4; i += THREADS) {
         const float4 x = S[i], z = R[i];
         y = fmaf(x.x, z.x, fmaf(x.y, z.y, fmaf(x.z, z.z, fmaf(x.w, z.w, y))));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    double carry = (double)y * p.scale;
-    const size_t plane = (size_t)BH * p.N;
-    const float *dot = p.dot + (size_t)bh * p.N;
-    for (int t = t1 - 1 - lane;; t -= 32) {          // lane 0 has the latest token
-        float d = 0.f, g = 0.f;
-        if (t >= t0) {
-            for (int k = 0; k < p.planes; ++k) d += dot[k * plane + t];
-            g = p.g[((size_t)b * p.N + t) * p.H + h];
-        }
+    if (lane == 0) sums[kGateTiles + warp] = y;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float up = __shfl_up_sync(0xffffffffu, d, o);
-            if (lane >= o) d += up;
+            const float up = __shfl_up_sync(0xffffffffu, d[i], o);
+            if (lane >= o) d[i] += up;
         }
-        if (t >= t0) p.dg[((size_t)b * p.N + t) * p.H + h] = g < RESET ? 0.f : (float)(carry + d);
-        carry += __shfl_sync(0xffffffffu, d, 31);
-        if (__shfl_sync(0xffffffffu, t, 31) <= t0) break;
+        if (lane == 31) sums[warp + WARPS * i] = d[i];
+    }
+    __syncthreads();
+    double carry = 0.0;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) carry += sums[kGateTiles + k];
+    carry *= p.scale;
+#pragma unroll
+    for (int k = 0; k < kGateTiles; ++k) {
+        if (k % WARPS == warp) {
+            const int i = k / WARPS, t = t1 - 1 - lane - 32 * k;
+            if (t >= t0) p.dg[((size_t)b * p.N + t) * p.H + h] = g[i] < RESET ? 0.f : (float)(carry + d[i]);
+        }
+        carry += sums[k];
     }
 }
 
@@ -285,19 +316,43 @@ struct Plan {
     size_t before, after, decays, dot, bytes;   // workspace offsets
 };
 
+template <int D>
+int slots(int dtype)
+{
+    return kSms * (dtype == LCLA_BF16 ? Shape<__nv_bfloat16, D>::BLOCKS : Shape<float, D>::BLOCKS);
+}
+
+// How many segments: the time of a tile step of all blocks on an SM grows with them once they hide its latency, so
+// the candidates are those that fill whole rounds of resident blocks; more segments than one cost the totals and the
+// scan.  All in microseconds, measured (constants below).
 Plan make_plan(int B, int H, int N, int d, int dtype, bool backward)
 {
     Plan p = {};
     if (N == 0 || (!backward && N <= kShort)) return p;
-    const int tiles = (N + TILE - 1) / TILE, ns = d / 32;
-    const long long warps = (long long)B * H * ns;
-    long long nseg = ((long long)kSms * 12 + warps - 1) / warps;
-    const int min_tiles = backward ? 4 : 8;
-    if (nseg > tiles / min_tiles) nseg = tiles / min_tiles;
-    if (nseg < 1) nseg = 1;
-    p.seg_tiles = (int)((tiles + nseg - 1) / nseg);
-    if (backward && p.seg_tiles > 32) p.seg_tiles = 32;
-    p.nseg = (tiles + p.seg_tiles - 1) / p.seg_tiles;
+    const int tiles = (N + TILE - 1) / TILE, ns = d / 32, G = WARPS / ns;
+    const long long per_seg = (long long)((H + G - 1) / G) * B * (backward ? 2 : 1);
+    const long long cap = d == 32 ? slots<32>(dtype) : slots<64>(dtype);
+    const double alone = 1.0, full = 2.2, fixed = 8.0;      // a tile step on an empty and a full SM; totals and scan
+    double best = 1e30;
+    p.nseg = 1;
+    p.seg_tiles = tiles;
+    for (int c = 0; c <= 16; ++c) {
+        long long nseg = c == 0 ? 1 : c * cap / per_seg;
+        if (nseg < 1 || (c && nseg == 1)) continue;
+        if (nseg > tiles) nseg = tiles;
+        long long ts = (tiles + nseg - 1) / nseg;
+        if (backward && ts > kGateTiles) ts = kGateTiles;
+        nseg = (tiles + ts - 1) / ts;
+        const long long blocks = nseg * per_seg, rounds = (blocks + cap - 1) / cap;
+        const double share = blocks >= cap ? 1.0 : (double)blocks / cap;
+        const double step = full * share > alone ? full * share : alone;
+        const double cost = rounds * (ts + 1.5) * step * (nseg > 1 ? 1.45 : 1.0) + (nseg > 1 ? fixed : 0.0);
+        if (cost < best) {
+            best = cost;
+            p.nseg = (int)nseg;
+            p.seg_tiles = (int)ts;
+        }
+    }
     const size_t slice = (size_t)B * H * d * d * sizeof(float);
     size_t at = 0;
     if (p.nseg > 1 || backward) {
@@ -324,7 +379,9 @@ int check_shape(int B, int H, int N, int d, int dtype)
     if (N > (1 << 30) || B > 65535 || H > 65535) return LCLA_ERR_UNSUPPORTED;
     // the state kernels count float4s of all heads' states, and the others blocks, in 32 bits
     if ((long long)B * H * d * d / 4 > 0x7ffffff0LL) return LCLA_ERR_UNSUPPORTED;
-    if ((long long)((N + 31) / 32) * H * 3 > 0x7fffffffLL) return LCLA_ERR_UNSUPPORTED;
+    if ((long long)((N + 31) / 32) * H * 2 > 0x7fffffffLL) return LCLA_ERR_UNSUPPORTED;
+    // and the gate gradient's blocks, one per head and segment of at most kGateTiles tiles
+    if ((long long)B * H * ((N + 31) / 32) > 0x7fffffffLL) return LCLA_ERR_UNSUPPORTED;
     return LCLA_OK;
 }
 
@@ -344,7 +401,7 @@ unsigned blocks(const Work &w, int roles)
 template <typename T, int D>
 void launch_totals(const Work &w, const Totals &t, int roles, cudaStream_t st)
 {
-    using S = Smem<T, D, 2, Ring<T, D>::TOTAL>;
+    using S = Smem<T, D, 2, Shape<T, D>::TOTAL_STAGES>;
     set_smem(gated_totals_k<T, D>, S::BYTES);
     gated_totals_k<T, D><<<dim3(blocks<D>(w, roles), w.B), THREADS, S::BYTES, st>>>(w, t, roles);
 }
@@ -385,9 +442,11 @@ int run_forward(const void *q, const void *k, const void *v, const Work &w, cons
         r.state = before;
         r.state_end = nullptr;
     }
-    using S = Smem<T, D, 3, Ring<T, D>::MAIN>;
-    set_smem(gated_forward_k<T, D>, S::BYTES);
-    gated_forward_k<T, D><<<dim3(blocks<D>(w, 1), w.B), THREADS, S::BYTES, st>>>(w, r);
+    using S = Smem<T, D, 3, Shape<T, D>::STAGES>;
+    constexpr int FEW = sizeof(T) == 2 ? 2 : 3;   // fp32 has one form
+    auto kernel = w.nseg > 1 ? gated_forward_k<T, D, FEW> : gated_forward_k<T, D, 3>;
+    set_smem(kernel, S::BYTES);
+    kernel<<<dim3(blocks<D>(w, 1), w.B), THREADS, S::BYTES, st>>>(w, r);
     return launched();
 }
 
@@ -418,22 +477,26 @@ int run_backward(const void *dout, const void *q, const void *k, const void *v, 
     const size_t plane = (size_t)BH * w.N;
     Roles rs = {};
     // recur reads the state of segment `seg` also where there is only one
-    rs.r[0].q = dout; rs.r[0].k = v; rs.r[0].v = k; rs.r[0].x = q; rs.r[0].out = dq;
-    rs.r[0].state = before; rs.r[0].dot = dot; rs.r[0].sign = 1.f;
-    rs.r[1].q = v; rs.r[1].k = dout; rs.r[1].v = q; rs.r[1].x = k; rs.r[1].out = dk;
-    rs.r[1].state = after; rs.r[1].dot = dot + ns * plane; rs.r[1].sign = -1.f;
-    rs.r[2].q = k; rs.r[2].k = q; rs.r[2].v = dout; rs.r[2].out = dv;
-    rs.r[2].state = after;
-    using S = Smem<T, D, 4, Ring<T, D>::MAIN>;
-    set_smem(gated_backward_k<T, D>, S::BYTES);
-    gated_backward_k<T, D><<<dim3(blocks<D>(w, 3), w.B), THREADS, S::BYTES, st>>>(w, rs);
+    Role &rq = rs.r[0], &rk = rs.r[1], rv = {};
+    rq.q = dout; rq.k = v; rq.v = k; rq.x = q; rq.out = dq;
+    rq.state = before; rq.transposed = true; rq.dot = dot; rq.sign = 1.f;
+    rk.q = v; rk.k = dout; rk.v = q; rk.x = k; rk.out = dk;
+    rk.state = after; rk.transposed = true; rk.dot = dot + ns * plane; rk.sign = -1.f;
+    rk.rev = true;
+    rv.q = k; rv.k = q; rv.v = dout; rv.out = dv;
+    rv.state = after; rv.rev = true;
+    using S4 = Smem<T, D, 4, Shape<T, D>::QK_STAGES>;
+    set_smem(gated_backward_qk_k<T, D>, S4::BYTES);
+    gated_backward_qk_k<T, D><<<dim3(blocks<D>(w, 2), w.B), THREADS, S4::BYTES, st>>>(w, rs);
+    using S3 = Smem<T, D, 3, Shape<T, D>::STAGES>;
+    set_smem(gated_backward_v_k<T, D>, S3::BYTES);
+    gated_backward_v_k<T, D><<<dim3(blocks<D>(w, 1), w.B), THREADS, S3::BYTES, st>>>(w, rv);
     GradGate gg = {};
     gg.g = w.g; gg.dot = dot; gg.before = before; gg.after = after; gg.dg = dg;
     gg.B = w.B; gg.H = w.H; gg.N = w.N; gg.nseg = w.nseg; gg.seg_tiles = w.seg_tiles;
     gg.planes = 2 * ns; gg.n4 = D * D / 4;
     gg.scale = w.scale;
-    const long long units = (long long)BH * w.nseg;
-    gated_dgate_k<<<(unsigned)((units + 3) / 4), 128, 0, st>>>(gg);
+    gated_dgate_k<<<(unsigned)((long long)BH * w.nseg), THREADS, 0, st>>>(gg);
     return launched();
 }
 

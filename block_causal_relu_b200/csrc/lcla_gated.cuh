@@ -84,30 +84,56 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
+// Two fp32 operations in one instruction: these kernels are bound by the instructions they issue.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; "
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 template <int NT>
-__device__ __forceinline__ void split(Co<__nv_bfloat16, NT> &o, float x, float y)
+__device__ __forceinline__ void split(Co<__nv_bfloat16, NT> &o, float2 v)
 {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        o.u[i] = pack_bf16(x, y);
-        if (i + 1 < NT) {
-            x -= lo_f(o.u[i]);
-            y -= hi_f(o.u[i]);
-        }
+        o.u[i] = pack_bf16(v.x, v.y);
+        if (i + 1 < NT) v = fma2(make_float2(lo_f(o.u[i]), hi_f(o.u[i])), both(-1.f), v);
     }
 }
 template <typename P>
-__device__ __forceinline__ void split_tf32(P &o, float x, float y)
+__device__ __forceinline__ void split_tf32(P &o, float2 v)
 {
-    o.h[0] = tf32(x);
-    o.h[1] = tf32(y);
-    o.l[0] = tf32(x - __uint_as_float(o.h[0]));
-    o.l[1] = tf32(y - __uint_as_float(o.h[1]));
+    o.h[0] = tf32(v.x);
+    o.h[1] = tf32(v.y);
+    const float2 l = fma2(make_float2(__uint_as_float(o.h[0]), __uint_as_float(o.h[1])), both(-1.f), v);
+    o.l[0] = tf32(l.x);
+    o.l[1] = tf32(l.y);
 }
 template <int NT>
-__device__ __forceinline__ void split(Co<float, NT> &o, float x, float y)
+__device__ __forceinline__ void split(Co<float, NT> &o, float2 v)
 {
-    split_tf32(o, x, y);
+    split_tf32(o, v);
 }
 __device__ __forceinline__ float2 value(const In<__nv_bfloat16> &p) { return make_float2(lo_f(p.u), hi_f(p.u)); }
 __device__ __forceinline__ float2 value(const In<float> &p)
@@ -116,68 +142,94 @@ __device__ __forceinline__ float2 value(const In<float> &p)
                        __uint_as_float(p.h[1]) + __uint_as_float(p.l[1]));
 }
 
+// ZERO: the sum starts from zero, which needs no registers to be cleared.
+template <bool ZERO>
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (ZERO)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+template <bool ZERO>
 __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (ZERO)
+        asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// c += A B over 16 entries of the contraction.  A's pairs: (row l/4, k 0-7), (row l/4 + 8, k 0-7), (row l/4, k 8-15),
-// (row l/4 + 8, k 8-15); B's: (k 0-7), (k 8-15) of column l/4.  The smallest products are added first.
-__device__ __forceinline__ void mma(float (&c)[4], const In<__nv_bfloat16> (&a)[4], const In<__nv_bfloat16> &b0,
+// c (+)= A B over 16 entries of the contraction, in STEPS instructions: products of the terms of A and B, the smallest
+// first.  A's pairs: (row l/4, k 0-7), (row l/4 + 8, k 0-7), (row l/4, k 8-15), (row l/4 + 8, k 8-15); B's: (k 0-7),
+// (k 8-15) of column l/4.  Callers take one step of several products in turn, so that no instruction waits for the one
+// before it.
+template <typename T, int NT>
+struct Steps {
+    static constexpr int N = sizeof(T) == 2 ? NT : 6;
+};
+template <bool ZERO>
+__device__ __forceinline__ void mma(int, float (&c)[4], const In<__nv_bfloat16> (&a)[4], const In<__nv_bfloat16> &b0,
                                     const In<__nv_bfloat16> &b1)
 {
-    mma_bf16(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u, b1.u);
+    mma_bf16<ZERO>(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u, b1.u);
 }
-template <int NT>
-__device__ __forceinline__ void mma(float (&c)[4], const Co<__nv_bfloat16, NT> (&a)[4], const In<__nv_bfloat16> &b0,
-                                    const In<__nv_bfloat16> &b1)
+template <bool ZERO, int NT>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const Co<__nv_bfloat16, NT> (&a)[4],
+                                    const In<__nv_bfloat16> &b0, const In<__nv_bfloat16> &b1)
 {
-#pragma unroll
-    for (int i = NT - 1; i >= 0; --i) mma_bf16(c, a[0].u[i], a[1].u[i], a[2].u[i], a[3].u[i], b0.u, b1.u);
+    const int i = NT - 1 - step;
+    mma_bf16<ZERO>(c, a[0].u[i], a[1].u[i], a[2].u[i], a[3].u[i], b0.u, b1.u);
 }
-template <int NT>
-__device__ __forceinline__ void mma(float (&c)[4], const In<__nv_bfloat16> (&a)[4], const Co<__nv_bfloat16, NT> &b0,
-                                    const Co<__nv_bfloat16, NT> &b1)
+template <bool ZERO, int NT>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const In<__nv_bfloat16> (&a)[4],
+                                    const Co<__nv_bfloat16, NT> &b0, const Co<__nv_bfloat16, NT> &b1)
 {
-#pragma unroll
-    for (int i = NT - 1; i >= 0; --i) mma_bf16(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u[i], b1.u[i]);
+    const int i = NT - 1 - step;
+    mma_bf16<ZERO>(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u[i], b1.u[i]);
 }
-template <typename PA, typename PB>
-__device__ __forceinline__ void mma_split(float (&c)[4], const PA (&a)[4], const PB &b0, const PB &b1)
+// A tf32 instruction contracts 8 entries: its slots 0-3 take the first of each pair, slots 4-7 the second.
+template <bool ZERO, typename PA, typename PB>
+__device__ __forceinline__ void mma_split(int step, float (&c)[4], const PA (&a)[4], const PB &b0, const PB &b1)
 {
-    // a tf32 instruction contracts 8 entries: slots 0-3 take the first of each pair, slots 4-7 the second
-    mma_tf32(c, a[0].l[0], a[1].l[0], a[0].l[1], a[1].l[1], b0.h[0], b0.h[1]);
-    mma_tf32(c, a[2].l[0], a[3].l[0], a[2].l[1], a[3].l[1], b1.h[0], b1.h[1]);
-    mma_tf32(c, a[0].h[0], a[1].h[0], a[0].h[1], a[1].h[1], b0.l[0], b0.l[1]);
-    mma_tf32(c, a[2].h[0], a[3].h[0], a[2].h[1], a[3].h[1], b1.l[0], b1.l[1]);
-    mma_tf32(c, a[0].h[0], a[1].h[0], a[0].h[1], a[1].h[1], b0.h[0], b0.h[1]);
-    mma_tf32(c, a[2].h[0], a[3].h[0], a[2].h[1], a[3].h[1], b1.h[0], b1.h[1]);
+    switch (step) {
+    case 0: return mma_tf32<ZERO>(c, a[0].l[0], a[1].l[0], a[0].l[1], a[1].l[1], b0.h[0], b0.h[1]);
+    case 1: return mma_tf32<false>(c, a[2].l[0], a[3].l[0], a[2].l[1], a[3].l[1], b1.h[0], b1.h[1]);
+    case 2: return mma_tf32<false>(c, a[0].h[0], a[1].h[0], a[0].h[1], a[1].h[1], b0.l[0], b0.l[1]);
+    case 3: return mma_tf32<false>(c, a[2].h[0], a[3].h[0], a[2].h[1], a[3].h[1], b1.l[0], b1.l[1]);
+    case 4: return mma_tf32<false>(c, a[0].h[0], a[1].h[0], a[0].h[1], a[1].h[1], b0.h[0], b0.h[1]);
+    default: return mma_tf32<false>(c, a[2].h[0], a[3].h[0], a[2].h[1], a[3].h[1], b1.h[0], b1.h[1]);
+    }
 }
-__device__ __forceinline__ void mma(float (&c)[4], const In<float> (&a)[4], const In<float> &b0, const In<float> &b1)
-{
-    mma_split(c, a, b0, b1);
-}
-template <int NT>
-__device__ __forceinline__ void mma(float (&c)[4], const Co<float, NT> (&a)[4], const In<float> &b0,
+template <bool ZERO>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const In<float> (&a)[4], const In<float> &b0,
                                     const In<float> &b1)
 {
-    mma_split(c, a, b0, b1);
+    mma_split<ZERO>(step, c, a, b0, b1);
 }
-template <int NT>
-__device__ __forceinline__ void mma(float (&c)[4], const In<float> (&a)[4], const Co<float, NT> &b0,
+template <bool ZERO, int NT>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const Co<float, NT> (&a)[4], const In<float> &b0,
+                                    const In<float> &b1)
+{
+    mma_split<ZERO>(step, c, a, b0, b1);
+}
+template <bool ZERO, int NT>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const In<float> (&a)[4], const Co<float, NT> &b0,
                                     const Co<float, NT> &b1)
 {
-    mma_split(c, a, b0, b1);
+    mma_split<ZERO>(step, c, a, b0, b1);
 }
 
 // -------------------------------------------------------- tiles in shared memory
@@ -243,7 +295,7 @@ __device__ __forceinline__ void load_a(In<float> (&a)[4], uint32_t tile, int m, 
     for (int p = 0; p < 4; ++p) {
         const int row = 16 * m + (lane >> 2) + 8 * (p & 1), col = 16 * ks + 8 * (p >> 1) + 2 * (lane & 3);
         const float2 v = lds2(tile + Tile<float, D>::at(row, col >> 2) + 4 * (col & 3));
-        split_tf32(a[p], v.x, v.y);
+        split_tf32(a[p], v);
     }
 }
 // B operands of two column tiles: columns are the rows 16 sb + [0, 16) of the tile, contraction over 16 ks + [0, 16).
@@ -262,7 +314,7 @@ __device__ __forceinline__ void load_b(In<float> (&b)[2][2], uint32_t tile, int 
         for (int p = 0; p < 2; ++p) {
             const int row = 16 * sb + 8 * n + (lane >> 2), col = 16 * ks + 8 * p + 2 * (lane & 3);
             const float2 v = lds2(tile + Tile<float, D>::at(row, col >> 2) + 4 * (col & 3));
-            split_tf32(b[n][p], v.x, v.y);
+            split_tf32(b[n][p], v);
         }
 }
 // Transposed: contraction over the rows 16 sb + [0, 16), entries 16 fb + [0, 16) as columns; t[fh][kh] holds entry
@@ -283,7 +335,7 @@ __device__ __forceinline__ void load_t(In<float> (&t)[2][2], uint32_t tile, int 
             const int row = 16 * sb + 8 * kh + 2 * (lane & 3), col = 16 * fb + 8 * fh + (lane >> 2);
             const float x = lds(tile + Tile<float, D>::at(row, col >> 2) + 4 * (col & 3));
             const float y = lds(tile + Tile<float, D>::at(row + 1, col >> 2) + 4 * (col & 3));
-            split_tf32(t[fh][kh], x, y);
+            split_tf32(t[fh][kh], make_float2(x, y));
         }
 }
 
@@ -297,6 +349,8 @@ struct Role {
     const float *state;      // state before each segment [nseg][B, H, d, d], or of the whole call (nseg = 1), or NULL (zero)
     float *state_end;        // nseg = 1: the state after the last token, or NULL
     float sign;
+    bool rev;                // the reversed recurrence
+    bool transposed;         // `state` lies [key][value]
 };
 
 struct Work {
@@ -307,14 +361,14 @@ struct Work {
 
 // Weights of a tile, per warp, in shared memory.
 struct Weights {
-    float2 split[TILE];      // whole part and fraction of G / ln 2 (negated in the reversed recurrence)
+    float whole[TILE];       // whole part and fraction of -G / ln 2 (of G / ln 2 in the reversed recurrence)
+    float frac[TILE];
     float in[TILE];          // weight of the carried state in each token's output
     float out[TILE];         // weight of each token in the next state
 };
 
 // Reads one log decay per lane; returns the decay of the whole tile and, in `total`, its G / ln 2.
-template <bool REV>
-__device__ __forceinline__ float tile_weights(Weights *w, float g, int lane, double &total)
+__device__ __forceinline__ float tile_weights(Weights *w, float g, bool rev, int lane, double &total)
 {
     double G = (double)(g < RESET ? RESET : g) * 1.4426950408889634;
 #pragma unroll
@@ -327,9 +381,10 @@ __device__ __forceinline__ float tile_weights(Weights *w, float g, int lane, dou
     const float a = (float)whole, b = (float)(G - whole);
     const float fromstart = ex2((float)G), toend = ex2((float)(end - G));
     __syncwarp();                          // the previous tile's weights have been read
-    w->split[lane] = REV ? make_float2(-a, -b) : make_float2(a, b);
-    w->in[lane] = REV ? toend : fromstart;
-    w->out[lane] = REV ? fromstart : toend;
+    w->whole[lane] = rev ? a : -a;
+    w->frac[lane] = rev ? b : -b;
+    w->in[lane] = rev ? toend : fromstart;
+    w->out[lane] = rev ? fromstart : toend;
     __syncwarp();
     total = end;
     return ex2((float)end);
@@ -351,6 +406,12 @@ __device__ __forceinline__ void copy_tile(uint32_t tile, const char *base, size_
     constexpr int RPI = NT / L::PIECES;                    // rows per step
     const int piece = tid % L::PIECES, r0 = tid / L::PIECES;
     const char *p = base + (size_t)(t0 + r0) * row_bytes + piece * 16;
+    if (t0 + TILE <= N) {
+#pragma unroll
+        for (int r = 0; r < TILE; r += RPI, p += RPI * row_bytes)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tile + L::at(r0 + r, piece)), "l"(p) : "memory");
+        return;
+    }
 #pragma unroll
     for (int r = 0; r < TILE; r += RPI, p += RPI * row_bytes) {
         const bool live = t0 + r0 + r < N;
@@ -386,31 +447,45 @@ __device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, uin
                 const float2 u = *reinterpret_cast<const float2 *>(&w->out[16 * sb + 8 * kh + 2 * (lane & 3)]);
 #pragma unroll
                 for (int fh = 0; fh < 2; ++fh) {
-                    const float2 x = value(v[fh][kh]);
-                    split(a[sb][2 * kh + fh], x.x * u.x, x.y * u.y);
+                    split(a[sb][2 * kh + fh], mul2(value(v[fh][kh]), u));
                 }
             }
         }
 #pragma unroll
-        for (int eb = 0; eb < D / 16; ++eb) {
-            In<T> k[2][2][2];
-            load_t<D>(k[0], kt, 0, eb, lane);
-            load_t<D>(k[1], kt, 1, eb, lane);
+        for (int e0 = 0; e0 < D / 16; e0 += 2) {         // 32 keys: four sums side by side
+            In<T> k[2][2][2][2];
+            float c[4][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma(c, a[0], k[0][n][0], k[0][n][1]);
-                mma(c, a[1], k[1][n][0], k[1][n][1]);
+            for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[m][2 * eb + n][i] = fmaf(S[m][2 * eb + n][i], decay, c[i]);
+                for (int e = 0; e < 2; ++e) load_t<D>(k[sb][e], kt, sb, e0 + e, lane);
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+                for (int i = 0; i < Steps<T, NT>::N; ++i)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const In<T>(&kk)[2] = k[sb][n >> 1][n & 1];
+                        if (sb == 0 && i == 0) mma<true>(i, c[n], a[sb], kk[0], kk[1]);
+                        else mma<false>(i, c[n], a[sb], kk[0], kk[1]);
+                    }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float(&st)[4] = S[m][2 * e0 + n];
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float2 r = fma2(make_float2(st[i], st[i + 1]), both(decay), make_float2(c[n][i], c[n][i + 1]));
+                    st[i] = r.x;
+                    st[i + 1] = r.y;
+                }
             }
         }
     }
 }
 
-// The warp's rows of a [d][d] state in global memory; TR: the state lies transposed ([key][value]).
-template <int D, bool TR>
-__device__ __forceinline__ void read_state(float (&S)[2][D / 8][4], const float *p, int slab, int lane)
+// The warp's rows of a [d][d] state in global memory.
+template <int D>
+__device__ __forceinline__ void read_state(float (&S)[2][D / 8][4], const float *p, bool transposed, int slab, int lane)
 {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -421,7 +496,7 @@ __device__ __forceinline__ void read_state(float (&S)[2][D / 8][4], const float 
                 const int c = 32 * slab + 16 * m + 8 * h + (lane >> 2), e = 8 * n + 2 * (lane & 3);
                 float2 v = make_float2(0.f, 0.f);
                 if (p) {
-                    if (TR) v = make_float2(p[e * D + c], p[(e + 1) * D + c]);
+                    if (transposed) v = make_float2(p[e * D + c], p[(e + 1) * D + c]);
                     else v = *reinterpret_cast<const float2 *>(p + c * D + e);
                 }
                 S[m][n][2 * h] = v.x;
@@ -479,9 +554,11 @@ __device__ __forceinline__ void write_rows<__nv_bfloat16>(__nv_bfloat16 *out, si
         }
 }
 
-// One recurrence over one segment of one head.  NP, NS_, NU: bf16 terms of the weighted scores, of the state where it
+enum Direction { FORWARD, REVERSED, EITHER };   // EITHER: the role says which, so that both run the same instructions
+
+// One recurrence over one segment of one head.  NP, NQ, NU: bf16 terms of the weighted scores, of the state where it
 // meets the query, and of the weighted values of an update.
-template <typename T, int D, bool REV, bool TR, bool DOT, int NP, int NQ, int NU, int STAGES>
+template <typename T, int D, Direction DIR, bool DOT, int NP, int NQ, int NU, int STAGES>
 __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h, int seg, int group, int slab, int lane,
                                       uint32_t ring, Weights *wt)
 {
@@ -490,6 +567,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
     const int tiles = (w.N + TILE - 1) / TILE;
     const int first = seg * w.seg_tiles, n = min(w.seg_tiles, tiles - first);
     if (n <= 0) return;
+    const bool rev = DIR == EITHER ? r.rev : DIR == REVERSED;
     const size_t row = (size_t)w.H * D, row_bytes = row * sizeof(T);
     const size_t at = (size_t)b * w.N * row + (size_t)h * D;
     const char *src[4] = {(const char *)((const T *)r.q + at), (const char *)((const T *)r.k + at),
@@ -497,7 +575,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
     const float *gp = w.g + (size_t)b * w.N * w.H + h;
     T *out = (T *)r.out + at + 32 * slab;
     const int tid = slab * 32 + lane;
-    auto tile_at = [&](int i) { return (REV ? first + n - 1 - i : first + i) * TILE; };
+    auto tile_at = [&](int i) { return (rev ? first + n - 1 - i : first + i) * TILE; };
     auto load = [&](int i) {
         if (i < n) {
             const uint32_t s = ring + (i % STAGES) * STAGE;
@@ -517,12 +595,12 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
     float S[2][D / 8][4];
     const float *st = r.state;
     if (st) st += (((size_t)(w.nseg > 1 ? seg : 0) * w.B + b) * w.H + h) * D * D;
-    read_state<D, TR>(S, st, slab, lane);
+    read_state<D>(S, st, DIR != FORWARD && r.transposed, slab, lane);
 
     for (int i = 0; i < n; ++i) {
         const float gnext = load_g(i + 1);
         double total;
-        const float decay = tile_weights<REV>(wt, g, lane, total);
+        const float decay = tile_weights(wt, g, rev, lane, total);
         g = gnext;
         wait_copies<STAGES - 2>();
         group_sync<NS>(group);               // this tile has landed for every warp, and the last one's slot is free
@@ -530,89 +608,109 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
         const uint32_t qt = ring + (i % STAGES) * STAGE, kt = qt + L::BYTES, vt = kt + L::BYTES, xt = vt + L::BYTES;
         const int t0 = tile_at(i);
 
+        // Query rows are taken 16 at a time, the block that sees one key block (itself) first: acc[m] holds the rows
+        // from 16 block(m) on.
+        auto block = [&](int m) { return rev ? 1 - m : m; };
         // the carried state's part of the outputs
         float acc[2][4][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int ks = 0; ks < D / 16; ++ks) {
+            In<T> a[2][4];
+            load_a<D>(a[0], qt, block(0), ks, lane);
+            load_a<D>(a[1], qt, block(1), ks, lane);
+            Co<T, NQ> s[4][2];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    const float(&x)[4] = S[c >> 1][2 * ks + e];
+                    split(s[c][e], make_float2(x[2 * (c & 1)], x[2 * (c & 1) + 1]));
+                }
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            In<T> a[2][4];
-            load_a<D>(a[0], qt, 0, ks, lane);
-            load_a<D>(a[1], qt, 1, ks, lane);
+            for (int j = 0; j < Steps<T, NQ>::N; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                Co<T, NQ> s0, s1;
-                split(s0, S[c >> 1][2 * ks][2 * (c & 1)], S[c >> 1][2 * ks][2 * (c & 1) + 1]);
-                split(s1, S[c >> 1][2 * ks + 1][2 * (c & 1)], S[c >> 1][2 * ks + 1][2 * (c & 1) + 1]);
-                mma(acc[0][c], a[0], s0, s1);
-                mma(acc[1][c], a[1], s0, s1);
-            }
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        if (ks == 0 && j == 0) mma<true>(j, acc[m][c], a[m], s[c][0], s[c][1]);
+                        else mma<false>(j, acc[m][c], a[m], s[c][0], s[c][1]);
+                    }
         }
-        // the tile's own part, 16 queries at a time
+        // the tile's own part
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            float2 gq[2];
+            const int row0 = 16 * block(m);
+            float2 gw[2], gf[2];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                const int t = 16 * m + 8 * hh + (lane >> 2);
-                gq[hh] = wt->split[t];
-                const float wi = wt->in[t];
+                const int t = row0 + 8 * hh + (lane >> 2);
+                gw[hh] = both(-wt->whole[t]);
+                gf[hh] = both(-wt->frac[t]);
+                const float2 wi = both(wt->in[t]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    acc[m][c][2 * hh] *= wi;
-                    acc[m][c][2 * hh + 1] *= wi;
+                    const float2 r = mul2(make_float2(acc[m][c][2 * hh], acc[m][c][2 * hh + 1]), wi);
+                    acc[m][c][2 * hh] = r.x;
+                    acc[m][c][2 * hh + 1] = r.y;
                 }
             }
 #pragma unroll
-            for (int sb = REV ? m : 0; sb <= (REV ? 1 : m); ++sb) {
-                float sc[2][4] = {};
+            for (int j = 0; j <= m; ++j) {
+                const int sb = block(j);
+                float sc[2][4];
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     In<T> a[4], k[2][2];
-                    load_a<D>(a, qt, m, ks, lane);
+                    load_a<D>(a, qt, block(m), ks, lane);
                     load_b<D>(k, kt, sb, ks, lane);
-                    mma(sc[0], a, k[0][0], k[0][1]);
-                    mma(sc[1], a, k[1][0], k[1][1]);
+#pragma unroll
+                    for (int i = 0; i < Steps<T, 1>::N; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            if (ks == 0 && i == 0) mma<true>(i, sc[nt], a, k[nt][0], k[nt][1]);
+                            else mma<false>(i, sc[nt], a, k[nt][0], k[nt][1]);
+                        }
                 }
                 Co<T, NP> p[4];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     const int s = 16 * sb + 8 * nt + 2 * (lane & 3);
-                    const float4 gk = *reinterpret_cast<const float4 *>(&wt->split[s]);
+                    const float2 kw = *reinterpret_cast<const float2 *>(&wt->whole[s]);
+                    const float2 kf = *reinterpret_cast<const float2 *>(&wt->frac[s]);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        const int t = 16 * m + 8 * hh + (lane >> 2);
-                        float x = sc[nt][2 * hh] * ex2((gq[hh].x - gk.x) + (gq[hh].y - gk.y));
-                        float y = sc[nt][2 * hh + 1] * ex2((gq[hh].x - gk.z) + (gq[hh].y - gk.w));
-                        if (sb == m) {
-                            x = (REV ? s >= t : s <= t) ? x : 0.f;
-                            y = (REV ? s + 1 >= t : s + 1 <= t) ? y : 0.f;
+                        const float2 e = add2(add2(gw[hh], kw), add2(gf[hh], kf));
+                        float2 x = mul2(make_float2(sc[nt][2 * hh], sc[nt][2 * hh + 1]), make_float2(ex2(e.x), ex2(e.y)));
+                        if (j == m) {          // key minus query, inside the block
+                            const int ahead = 8 * (nt - hh) + 2 * (lane & 3) - (lane >> 2);
+                            x.x = (rev ? ahead >= 0 : ahead <= 0) ? x.x : 0.f;
+                            x.y = (rev ? ahead >= -1 : ahead <= -1) ? x.y : 0.f;
                         }
-                        split(p[2 * nt + hh], x, y);
+                        split(p[2 * nt + hh], x);
                     }
                 }
+                In<T> v[2][2][2];
 #pragma unroll
-                for (int cb = 0; cb < 2; ++cb) {
-                    In<T> v[2][2];
-                    load_t<D>(v, vt, sb, 2 * slab + cb, lane);
-                    mma(acc[m][2 * cb], p, v[0][0], v[0][1]);
-                    mma(acc[m][2 * cb + 1], p, v[1][0], v[1][1]);
-                }
+                for (int cb = 0; cb < 2; ++cb) load_t<D>(v[cb], vt, sb, 2 * slab + cb, lane);
+#pragma unroll
+                for (int i = 0; i < Steps<T, NP>::N; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mma<false>(i, acc[m][c], p, v[c >> 1][c & 1][0], v[c >> 1][c & 1][1]);
             }
-            const int t = t0 + 16 * m + (lane >> 2);
+            const int t = t0 + row0 + (lane >> 2);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][c][j] *= w.scale;
+                for (int j = 0; j < 4; j += 2) {
+                    const float2 r = mul2(make_float2(acc[m][c][j], acc[m][c][j + 1]), both(w.scale));
+                    acc[m][c][j] = r.x;
+                    acc[m][c][j + 1] = r.y;
+                }
             if (DOT) {
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     float s = 0.f;
-                    const int rr = 16 * m + 8 * hh + (lane >> 2);
+                    const int rr = row0 + 8 * hh + (lane >> 2);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int col = 32 * slab + 8 * c + 2 * (lane & 3);
@@ -641,9 +739,9 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
 }
 
 // What a segment adds to the state, from zero, and its decay.
-template <typename T, int D, bool REV, int STAGES>
-__device__ __forceinline__ void total(const Work &w, const void *key, const void *val, float *part, float *decays, int b,
-                                      int h, int seg, int group, int slab, int lane, uint32_t ring, Weights *wt)
+template <typename T, int D, int NT, int STAGES>
+__device__ __forceinline__ void total(const Work &w, const void *key, const void *val, float *part, float *decays, bool rev,
+                                      int b, int h, int seg, int group, int slab, int lane, uint32_t ring, Weights *wt)
 {
     using L = Tile<T, D>;
     constexpr int NS = D / 32, STAGE = 2 * L::BYTES;
@@ -654,7 +752,7 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
     const char *kp = (const char *)((const T *)key + at), *vp = (const char *)((const T *)val + at);
     const float *gp = w.g + (size_t)b * w.N * w.H + h;
     const int tid = slab * 32 + lane;
-    auto tile_at = [&](int i) { return (REV ? first + n - 1 - i : first + i) * TILE; };
+    auto tile_at = [&](int i) { return (rev ? first + n - 1 - i : first + i) * TILE; };
     auto load = [&](int i) {
         if (i < n) {
             const uint32_t s = ring + (i % STAGES) * STAGE;
@@ -675,14 +773,14 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
     for (int i = 0; i < n; ++i) {
         const float gnext = load_g(i + 1);
         double t;
-        const float decay = tile_weights<REV>(wt, g, lane, t);
+        const float decay = tile_weights(wt, g, rev, lane, t);
         sum += t;
         g = gnext;
         wait_copies<STAGES - 2>();
         group_sync<NS>(group);
         load(i + STAGES - 1);
         const uint32_t kt = ring + (i % STAGES) * STAGE;
-        update<T, D, 3>(S, kt, kt + L::BYTES, wt, slab, decay, lane);
+        update<T, D, NT>(S, kt, kt + L::BYTES, wt, slab, decay, lane);
     }
     wait_copies<0>();
     const size_t at_s = ((size_t)seg * w.B + b) * w.H + h;
