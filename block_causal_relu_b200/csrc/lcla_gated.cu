@@ -24,6 +24,10 @@ using namespace lcla::gated;
 constexpr int kSms = 148;
 
 // ---------------------------------------------------------------- kernels
+// Kernels of a call after its first are launched while the one before them drains (launch_after); they read what it
+// wrote only after this.  Every kernel of a call waits so, hence each starts after all before its predecessor.
+__device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct Place {
     int b, h, seg, role, group, slab, lane;
     bool live;
@@ -73,7 +77,7 @@ struct Shape {
     static constexpr int STAGES = sizeof(T) == 2 && D == 64 ? 3 : 2;
     static constexpr int QK_STAGES = 2;
     static constexpr int TOTAL_BLOCKS = BLOCKS;
-    static constexpr int TOTAL_STAGES = STAGES + 1;
+    static constexpr int TOTAL_STAGES = 3;
 };
 
 // NU: terms of a state update.  Where the state after the call comes out of the scan, the state in here only meets
@@ -147,9 +151,10 @@ struct Scan {
     int nseg, BH, n4;          // n4: float4s of a state
 };
 
-// One thread per float4 of a state; the segments' values are read 8 at a time ahead of the chain.
+// One thread per float4 of a state; the segments' values are read 16 at a time ahead of the chain.
 __global__ void __launch_bounds__(128) gated_scan_k(const __grid_constant__ Scan s)
 {
+    after_launch_before();
     const int i = blockIdx.x * 128 + threadIdx.x, dir = blockIdx.y;
     const int all = s.BH * s.n4;
     if (i >= all) return;
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(128) gated_scan_k(const __grid_constant__ Scan
         c.x *= m; c.y *= m; c.z *= m; c.w *= m;
     }
     float4 *part = reinterpret_cast<float4 *>(s.part[dir]);
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int k0 = 0; k0 < s.nseg; k0 += U) {
         float4 v[U];
         float d[U];
@@ -198,7 +203,7 @@ struct GradGate {
     const float *before;       // [nseg + 1][B, H, d, d]: the state before each segment, and after the last
     const float *after;        // [nseg][B, H, d, d]: its gradient after each segment, over scale
     float *dg;
-    int B, H, N, nseg, seg_tiles, planes, n4;
+    int B, H, N, nseg, seg_tiles;
     float scale;
 };
 
@@ -207,8 +212,11 @@ struct GradGate {
 // each segment's end keeps it to 32-bit accuracy.  One block per segment of a head (at most 32 tiles): each warp takes
 // every fourth tile, latest first, reads all of them at once and sums each from its end.
 constexpr int kGateTiles = 32;     // tiles of a segment at most
+template <int D>
 __global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__ GradGate p)
 {
+    constexpr int PLANES = 2 * (D / 32), N4 = D * D / 4;
+    after_launch_before();
     constexpr int PER = kGateTiles / WARPS;
     __shared__ float sums[kGateTiles + WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = p.B * p.H;
@@ -220,18 +228,22 @@ __global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int t = t1 - 1 - lane - 32 * (warp + WARPS * i);    // lane 0 has the latest token
-        d[i] = g[i] = 0.f;
-        if (t >= t0) {
-            d[i] = dot[t];
-            for (int k = 1; k < p.planes; ++k) d[i] += dot[k * plane + t];
-            g[i] = p.g[((size_t)b * p.N + t) * p.H + h];
-        }
+        const int u = max(t, t0);                                 // loads without branches go out together
+        float v[PLANES];
+#pragma unroll
+        for (int k = 0; k < PLANES; ++k) v[k] = dot[k * plane + u];
+        g[i] = p.g[((size_t)b * p.N + u) * p.H + h];
+        d[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < PLANES; ++k) d[i] += v[k];
+        if (t < t0) d[i] = 0.f;
     }
-    const float4 *S = reinterpret_cast<const float4 *>(p.before) + ((size_t)(seg + 1) * BH + bh) * p.n4;
-    const float4 *R = reinterpret_cast<const float4 *>(p.after) + ((size_t)seg * BH + bh) * p.n4;
+    const float4 *S = reinterpret_cast<const float4 *>(p.before) + ((size_t)(seg + 1) * BH + bh) * N4;
+    const float4 *R = reinterpret_cast<const float4 *>(p.after) + ((size_t)seg * BH + bh) * N4;
     float y = 0.f;
-    for (int i = threadIdx.x; i < p.n4; i += THREADS) {
-        const float4 x = S[i], z = R[i];
+#pragma unroll
+    for (int i = 0; i < N4 / THREADS; ++i) {
+        const float4 x = S[threadIdx.x + i * THREADS], z = R[threadIdx.x + i * THREADS];
         y = fmaf(x.x, z.x, fmaf(x.y, z.y, fmaf(x.z, z.z, fmaf(x.w, z.w, y))));
     }
 #pragma unroll
@@ -391,6 +403,22 @@ void set_smem(F *kernel, int bytes)
     cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+template <typename... KArgs, typename... Args>
+void launch_after(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 template <int D>
 unsigned blocks(const Work &w, int roles)
 {
@@ -408,7 +436,7 @@ void launch_totals(const Work &w, const Totals &t, int roles, cudaStream_t st)
 
 void launch_scan(const Scan &s, int dirs, cudaStream_t st)
 {
-    gated_scan_k<<<dim3((s.BH * s.n4 + 127) / 128, dirs), 128, 0, st>>>(s);
+    launch_after(gated_scan_k, dim3((s.BH * s.n4 + 127) / 128, dirs), 128, 0, st, s);
 }
 
 template <typename T, int D>
@@ -446,7 +474,9 @@ int run_forward(const void *q, const void *k, const void *v, const Work &w, cons
     constexpr int FEW = sizeof(T) == 2 ? 2 : 3;   // fp32 has one form
     auto kernel = w.nseg > 1 ? gated_forward_k<T, D, FEW> : gated_forward_k<T, D, 3>;
     set_smem(kernel, S::BYTES);
-    kernel<<<dim3(blocks<D>(w, 1), w.B), THREADS, S::BYTES, st>>>(w, r);
+    const dim3 grid(blocks<D>(w, 1), w.B);
+    if (w.nseg > 1) launch_after(kernel, grid, THREADS, S::BYTES, st, w, r);
+    else kernel<<<grid, THREADS, S::BYTES, st>>>(w, r);
     return launched();
 }
 
@@ -487,16 +517,15 @@ int run_backward(const void *dout, const void *q, const void *k, const void *v, 
     rv.state = after; rv.rev = true;
     using S4 = Smem<T, D, 4, Shape<T, D>::QK_STAGES>;
     set_smem(gated_backward_qk_k<T, D>, S4::BYTES);
-    gated_backward_qk_k<T, D><<<dim3(blocks<D>(w, 2), w.B), THREADS, S4::BYTES, st>>>(w, rs);
+    launch_after(gated_backward_qk_k<T, D>, dim3(blocks<D>(w, 2), w.B), THREADS, S4::BYTES, st, w, rs);
     using S3 = Smem<T, D, 3, Shape<T, D>::STAGES>;
     set_smem(gated_backward_v_k<T, D>, S3::BYTES);
-    gated_backward_v_k<T, D><<<dim3(blocks<D>(w, 1), w.B), THREADS, S3::BYTES, st>>>(w, rv);
+    launch_after(gated_backward_v_k<T, D>, dim3(blocks<D>(w, 1), w.B), THREADS, S3::BYTES, st, w, rv);
     GradGate gg = {};
     gg.g = w.g; gg.dot = dot; gg.before = before; gg.after = after; gg.dg = dg;
     gg.B = w.B; gg.H = w.H; gg.N = w.N; gg.nseg = w.nseg; gg.seg_tiles = w.seg_tiles;
-    gg.planes = 2 * ns; gg.n4 = D * D / 4;
     gg.scale = w.scale;
-    gated_dgate_k<<<(unsigned)((long long)BH * w.nseg), THREADS, 0, st>>>(gg);
+    launch_after(gated_dgate_k<D>, dim3((unsigned)((long long)BH * w.nseg)), THREADS, 0, st, gg);
     return launched();
 }
 

@@ -32,6 +32,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "lcla_f32x2.cuh"
+
 namespace lcla {
 namespace gated {
 
@@ -83,34 +85,6 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
-// Two fp32 operations in one instruction: these kernels are bound by the instructions they issue.
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{.reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{.reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 r;
-    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; "
-        "mov.b64 {%0, %1}, d;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 template <int NT>
 __device__ __forceinline__ void split(Co<__nv_bfloat16, NT> &o, float2 v)
@@ -592,6 +566,8 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
     for (int i = 0; i < STAGES - 1; ++i) load(i);
     float g = load_g(0);
 
+    // The inputs above were there before the call; the states come from the kernel before this one.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float S[2][D / 8][4];
     const float *st = r.state;
     if (st) st += (((size_t)(w.nseg > 1 ? seg : 0) * w.B + b) * w.H + h) * D * D;

@@ -18,23 +18,40 @@
 #include <stdint.h>
 
 #include "lcla.h"
+#include "lcla_f32x2.cuh"
 #include "lcla_host.h"
 
 namespace {
 
+using namespace lcla;
 using namespace lcla::host;
 
 // ------------------------------------------------------------------ tables
 constexpr int kMaxPairs = 128;
 constexpr int kMaxAxes = 3;
 constexpr int kTabThreads = 256;
-constexpr int kTabVec = 4;         // consecutive table entries per thread
+constexpr int kTabTokens = 4;      // tokens per thread
+
+// Division of 0 <= n < 2^31 by a constant (Granlund and Montgomery, "Division by Invariant Integers using
+// Multiplication"): n / d = (high 32 bits of n m, plus n) >> s.
+struct Divisor {
+    unsigned d, m, s;
+};
+Divisor make_divisor(unsigned d)
+{
+    unsigned s = 0;
+    while ((1ull << s) < d) ++s;
+    return Divisor{d, (unsigned)((((1ull << s) - d) << 32) / d + 1), s};
+}
+__device__ __forceinline__ unsigned divide(unsigned n, const Divisor &d) { return (__umulhi(n, d.m) + n) >> d.s; }
 
 struct TabPlan {
     unsigned long long freq[kMaxPairs];   // revolutions per position, times 2^64
     unsigned char axis[kMaxPairs];
     long long first;
     long long extent[kMaxAxes];           // extent[a]: how far axis a counts (a >= 1)
+    Divisor by[kMaxAxes];                 // the same as divisors, where they and all indices are below 2^31
+    bool narrow;
     int axes, pairs, N;
     float amp;
 };
@@ -51,71 +68,83 @@ __device__ __forceinline__ void sincos_eighth(long long r, float &s, float &c)
     c = fmaf(y, c, 1.f);
 }
 
-__device__ __forceinline__ unsigned long long token_position(const TabPlan &p, const long long *positions, int a, int n)
-{
-    if (positions) return (unsigned long long)positions[(size_t)a * p.N + n];
-    const long long at = p.first + n;
-    if (p.axes == 1) return (unsigned long long)at;
-    if ((unsigned long long)at < (1ull << 31)) {   // 32-bit divisions: a third of the cost of 64-bit ones
-        unsigned m = (unsigned)at;
-        for (int i = p.axes - 1; i > a; --i) m /= (unsigned)p.extent[i];
-        return a ? m % (unsigned)p.extent[a] : m;
-    }
-    long long m = at;
-    for (int i = p.axes - 1; i > a; --i) m /= p.extent[i];
-    return (unsigned long long)(a ? m % p.extent[a] : m);
-}
-
-// One thread writes four consecutive entries of both tables, 16 bytes each.
+// Bound by its stores once the index arithmetic is out of the way (a first version with divisions and table reads for
+// every four entries took 57 us for the minute-scale latent's 108.6 MB).  A thread keeps VEC entries' frequencies in
+// registers and writes them for kTabTokens tokens; a block covers 256 / (pairs / VEC) tokens at a time.
+template <int VEC>
 __global__ void __launch_bounds__(kTabThreads)
 rotary_tables_k(const __grid_constant__ TabPlan p, const long long *__restrict__ positions, float *__restrict__ cosv,
                 float *__restrict__ sinv)
 {
-    __shared__ unsigned long long freq[kMaxPairs];   // threads of a warp want different entries
-    __shared__ unsigned char axis[kMaxPairs];
-    for (int i = threadIdx.x; i < p.pairs; i += kTabThreads) {
-        freq[i] = p.freq[i];
-        axis[i] = p.axis[i];
-    }
-    __syncthreads();
-    const long long total = (long long)p.N * p.pairs;
-    const long long at = ((long long)blockIdx.x * kTabThreads + threadIdx.x) * kTabVec;
-    if (at >= total) return;
-    int n = (int)(at / p.pairs), j = (int)(at - (long long)n * p.pairs);
-    int a = -1;
-    unsigned long long pos = 0;
-    float c[kTabVec], s[kTabVec];
+    const int groups = p.pairs / VEC, rows = kTabThreads / groups;
+    const int row = threadIdx.x / groups, j = (threadIdx.x - row * groups) * VEC;
+    if (row >= rows) return;
+    unsigned long long freq[VEC];
+    int axis[VEC];
 #pragma unroll
-    for (int i = 0; i < kTabVec; ++i) {
-        if (at + i < total) {
-            if (axis[j] != a) {
-                a = axis[j];
-                pos = token_position(p, positions, a, n);
-            }
-            const unsigned long long turn = pos * freq[j];
-            const unsigned quad = (unsigned)((turn + (1ull << 61)) >> 62);
-            float sn, cs;
-            sincos_eighth((long long)(turn - ((unsigned long long)quad << 62)), sn, cs);
-            const float x = (quad & 1) ? -sn : cs, y = (quad & 1) ? cs : sn;
-            c[i] = ((quad & 2) ? -x : x) * p.amp;
-            s[i] = ((quad & 2) ? -y : y) * p.amp;
-            if (++j == p.pairs) {
-                j = 0;
-                ++n;
-                a = -1;
-            }
+    for (int i = 0; i < VEC; ++i) {
+        freq[i] = p.freq[j + i];
+        axis[i] = p.axis[j + i];
+    }
+    const int n0 = (int)((long long)blockIdx.x * rows * kTabTokens) + row;
+    unsigned long long given[kTabTokens][kMaxAxes];
+    if (positions) {
+#pragma unroll
+        for (int k = 0; k < kTabTokens; ++k)
+#pragma unroll
+            for (int a = 0; a < kMaxAxes; ++a)
+                given[k][a] = a < p.axes ? (unsigned long long)positions[(size_t)a * p.N + min(n0 + k * rows, p.N - 1)] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kTabTokens; ++k) {
+        const int n = n0 + k * rows;
+        if (n >= p.N) return;
+        unsigned long long pos[kMaxAxes] = {0, 0, 0};
+        if (positions) {
+#pragma unroll
+            for (int a = 0; a < kMaxAxes; ++a) pos[a] = given[k][a];
+        } else if (p.narrow) {
+            unsigned m = (unsigned)(p.first + n);
+#pragma unroll
+            for (int a = kMaxAxes - 1; a > 0; --a)
+                if (a < p.axes) {
+                    const unsigned q = divide(m, p.by[a]);
+                    pos[a] = m - q * p.by[a].d;
+                    m = q;
+                }
+            pos[0] = m;
+        } else {
+            long long m = p.first + n;
+#pragma unroll
+            for (int a = kMaxAxes - 1; a > 0; --a)
+                if (a < p.axes) {
+                    const long long q = m / p.extent[a];
+                    pos[a] = (unsigned long long)(m - q * p.extent[a]);
+                    m = q;
+                }
+            pos[0] = (unsigned long long)m;
         }
-    }
-    if (at + kTabVec <= total) {
-        *reinterpret_cast<float4 *>(cosv + at) = make_float4(c[0], c[1], c[2], c[3]);
-        *reinterpret_cast<float4 *>(sinv + at) = make_float4(s[0], s[1], s[2], s[3]);
-    } else {
+        float c[VEC], s[VEC];
 #pragma unroll
-        for (int i = 0; i < kTabVec; ++i)
-            if (at + i < total) {
-                cosv[at + i] = c[i];
-                sinv[at + i] = s[i];
-            }
+        for (int i = 0; i < VEC; ++i) {
+            const unsigned long long turn = (axis[i] == 0 ? pos[0] : axis[i] == 1 ? pos[1] : pos[2]) * freq[i];
+            // the nearest quarter turn, and what is left
+            const unsigned high = (unsigned)(turn >> 32), quad = (high + 0x20000000u) >> 30;
+            const unsigned left = high - (quad << 30);
+            float sn, cs;
+            sincos_eighth((long long)(((unsigned long long)left << 32) | (unsigned)turn), sn, cs);
+            const unsigned x = __float_as_uint((quad & 1) ? sn : cs), y = __float_as_uint((quad & 1) ? cs : sn);
+            c[i] = __uint_as_float(x ^ (((quad + 1) << 30) & 0x80000000u)) * p.amp;   // quarters 1 and 2
+            s[i] = __uint_as_float(y ^ ((quad << 30) & 0x80000000u)) * p.amp;         // quarters 2 and 3
+        }
+        const size_t at = (size_t)n * p.pairs + j;
+        if (VEC == 4) {
+            *reinterpret_cast<float4 *>(cosv + at) = make_float4(c[0], c[VEC > 1], c[VEC / 2], c[VEC - 1]);
+            *reinterpret_cast<float4 *>(sinv + at) = make_float4(s[0], s[VEC > 1], s[VEC / 2], s[VEC - 1]);
+        } else {
+            cosv[at] = c[0];
+            sinv[at] = s[0];
+        }
     }
 }
 
@@ -123,6 +152,7 @@ rotary_tables_k(const __grid_constant__ TabPlan p, const long long *__restrict__
 constexpr int kVec = 8;            // entries of a row per lane
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kReads = 5;          // reads of a unit of the forward
 
 struct View {                      // rows of one tensor: token t, head h at p + t * ld + h * d
     const void *p;
@@ -139,126 +169,177 @@ struct NormArgs {
     float *part;                   // gradient: [ctas][d] per side, queries' CTAs first
     long long T;                   // tokens, B * N
     int N, P, d, rd, heads[2], units[2], ctas[2];
+    int span[2];                   // gradient: reads that a warp takes of a token at a time
     float eps, inv_d;
 };
 
-template <typename T>
-struct Row8;
-template <>
-struct Row8<float> {
-    float4 a, b;
-    __device__ void load(const float *p)
-    {
-        a = reinterpret_cast<const float4 *>(p)[0];
-        b = reinterpret_cast<const float4 *>(p)[1];
-    }
-    __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ void get(float (&x)[kVec]) const
-    {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
+// A lane's 8 entries of a row as two pairs of even and two of odd ones, for packed arithmetic.
+struct Eight {
+    float2 e[2], o[2];             // e[j] = entries 4j, 4j + 2; o[j] = entries 4j + 1, 4j + 3
 };
-template <>
-struct Row8<__nv_bfloat16> {
-    uint4 u;
-    __device__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
-    __device__ void zero() { u = make_uint4(0, 0, 0, 0); }
-    __device__ void get(float (&x)[kVec]) const
+__device__ __forceinline__ Eight zeros() { return Eight{{both(0.f), both(0.f)}, {both(0.f), both(0.f)}}; }
+__device__ __forceinline__ float total(const Eight &a)
+{
+    const float2 s = add2(add2(a.e[0], a.e[1]), add2(a.o[0], a.o[1]));
+    return s.x + s.y;
+}
+__device__ __forceinline__ Eight times(const Eight &a, const Eight &b)
+{
+    return Eight{{mul2(a.e[0], b.e[0]), mul2(a.e[1], b.e[1])}, {mul2(a.o[0], b.o[0]), mul2(a.o[1], b.o[1])}};
+}
+__device__ __forceinline__ Eight times(const Eight &a, float s)
+{
+    const float2 b = both(s);
+    return Eight{{mul2(a.e[0], b), mul2(a.e[1], b)}, {mul2(a.o[0], b), mul2(a.o[1], b)}};
+}
+__device__ __forceinline__ Eight plus_times(const Eight &a, const Eight &b, const Eight &c)   // a b + c
+{
+    return Eight{{fma2(a.e[0], b.e[0], c.e[0]), fma2(a.e[1], b.e[1], c.e[1])},
+                 {fma2(a.o[0], b.o[0], c.o[0]), fma2(a.o[1], b.o[1], c.o[1])}};
+}
+__device__ __forceinline__ Eight plus_times(const Eight &a, float s, const Eight &c)
+{
+    const float2 b = both(s);
+    return Eight{{fma2(a.e[0], b, c.e[0]), fma2(a.e[1], b, c.e[1])}, {fma2(a.o[0], b, c.o[0]), fma2(a.o[1], b, c.o[1])}};
+}
+
+// The same entries as they lie in memory.
+template <typename T>
+struct Raw {
+    static constexpr int WORDS = 2 * (int)sizeof(T);
+    uint32_t w[WORDS];
+    __device__ void load(const T *p)
     {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int i = 0; i < WORDS; i += 4) {
+            const uint4 u = reinterpret_cast<const uint4 *>(p)[i / 4];
+            w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
         }
     }
-};
-__device__ __forceinline__ void store8(float *p, const float (&x)[kVec])
-{
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[kVec])
-{
-    uint32_t w[4];
+    __device__ void store(T *p) const
+    {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int i = 0; i < WORDS; i += 4) reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ Raw from_lane(int lane) const   // every lane of the warp takes part
+    {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], lane);
+        return r;
+    }
+    __device__ Eight get() const
+    {
+        Eight x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (sizeof(T) == 2) {
+                const uint32_t a = w[2 * j], b = w[2 * j + 1];
+                x.e[j] = make_float2(__uint_as_float(a << 16), __uint_as_float(b << 16));
+                x.o[j] = make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u));
+            } else {
+                const uint32_t *v = w + (4 * j) % WORDS;
+                x.e[j] = make_float2(__uint_as_float(v[0]), __uint_as_float(v[2]));
+                x.o[j] = make_float2(__uint_as_float(v[1]), __uint_as_float(v[3]));
+            }
+        }
+        return x;
+    }
+    __device__ void set(const Eight &x)
+    {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (sizeof(T) == 2) {
+                w[2 * j] = pack(x.e[j].x, x.o[j].x);
+                w[2 * j + 1] = pack(x.e[j].y, x.o[j].y);
+            } else {
+                uint32_t *v = w + (4 * j) % WORDS;
+                v[0] = __float_as_uint(x.e[j].x);
+                v[1] = __float_as_uint(x.o[j].x);
+                v[2] = __float_as_uint(x.e[j].y);
+                v[3] = __float_as_uint(x.o[j].y);
+            }
+        }
+    }
+    __device__ static uint32_t pack(float lo, float hi)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+// Entries [at, at + 8) of a fp32 array, or `fill` without it.
+__device__ __forceinline__ Eight eight_of(const float *p, int at, bool on, float fill)
+{
+    float v[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = fill;
+    if (p && on) {
+        const float4 a = reinterpret_cast<const float4 *>(p + at)[0], b = reinterpret_cast<const float4 *>(p + at)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    return Eight{{make_float2(v[0], v[2]), make_float2(v[4], v[6])}, {make_float2(v[1], v[3]), make_float2(v[5], v[7])}};
 }
 
-// The rotation of a lane's entries [8 l, 8 l + 8): its factors, kept for all rows of a token.
+// Each entry of R x (or R^T x) is c x + s x', x' the other entry of its pair: in the same lane (interleaved) or in lane
+// `partner` (half layout).  c and s serve all rows of a token.
 template <bool HALF>
 struct Turn {
-    static constexpr int NF = HALF ? kVec : kVec / 2;
-    float c[NF], s[NF];
-    int partner;        // HALF: the lane that holds the other entry of each pair
-    bool on;            // HALF: this lane's entries are turned
+    Eight c, s;
 
-    __device__ void load(const NormArgs &a, long long token, int l, int lane)
+    __device__ static int partner(const NormArgs &a, int l, int lane)
+    {
+        const int per = a.rd / 2 / kVec;            // lanes per half
+        return !HALF || kVec * l >= a.rd ? lane : l >= per ? lane - per : lane + per;
+    }
+    // sign +1: R, -1: R^T
+    __device__ void load(const NormArgs &a, long long token, int l, float sign)
     {
         long long row = a.positions ? a.positions[token] : (unsigned)token % (unsigned)a.N;
         row = row < 0 ? 0 : row >= a.P ? a.P - 1 : row;   // a bad position reads a wrong row, never out of bounds
         const int hp = a.rd / 2;
         const float *pc = a.cosv + row * hp, *ps = a.sinv + row * hp;
-        partner = lane;
         if (HALF) {
-            const int at = kVec * l, per = hp / kVec;     // lanes per half
-            on = at < a.rd;
-            const bool second = l >= per;
-            const int p0 = second ? at - hp : at;
-            if (on) partner = second ? lane - per : lane + per;
-#pragma unroll
-            for (int j = 0; j < NF; j += 4) {
-                const float4 u = on ? *reinterpret_cast<const float4 *>(pc + p0 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
-                const float4 v = on ? *reinterpret_cast<const float4 *>(ps + p0 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                c[j] = u.x; c[j + 1] = u.y; c[j + 2] = u.z; c[j + 3] = u.w;
-                // first half: x c - x' s; second half: x c + x' s
-                s[j] = second ? v.x : -v.x;
-                s[j + 1] = second ? v.y : -v.y;
-                s[j + 2] = second ? v.z : -v.z;
-                s[j + 3] = second ? v.w : -v.w;
-            }
+            const bool on = kVec * l < a.rd, second = kVec * l >= hp;
+            const int p0 = second ? kVec * l - hp : kVec * l;
+            c = eight_of(pc, p0, on, 1.f);
+            s = times(eight_of(ps, p0, on, 0.f), second ? sign : -sign);
         } else {
-            const int p0 = NF * l;
-            on = 2 * p0 < a.rd;
+            const int p0 = kVec / 2 * l;
+            float4 u = make_float4(1.f, 1.f, 1.f, 1.f), v = make_float4(0.f, 0.f, 0.f, 0.f);
             if ((hp & 3) == 0) {                          // whole 16-byte pieces of aligned table rows
-                const float4 u = on ? *reinterpret_cast<const float4 *>(pc + p0) : make_float4(1.f, 1.f, 1.f, 1.f);
-                const float4 v = on ? *reinterpret_cast<const float4 *>(ps + p0) : make_float4(0.f, 0.f, 0.f, 0.f);
-                c[0] = u.x; c[1] = u.y; c[2] = u.z; c[3] = u.w;
-                s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < NF; ++j) {
-                    c[j] = p0 + j < hp ? pc[p0 + j] : 1.f;
-                    s[j] = p0 + j < hp ? ps[p0 + j] : 0.f;
+                if (p0 < hp) {
+                    u = *reinterpret_cast<const float4 *>(pc + p0);
+                    v = *reinterpret_cast<const float4 *>(ps + p0);
                 }
+            } else {
+                if (p0 < hp) { u.x = pc[p0]; v.x = ps[p0]; }
+                if (p0 + 1 < hp) { u.y = pc[p0 + 1]; v.y = ps[p0 + 1]; }
+                if (p0 + 2 < hp) { u.z = pc[p0 + 2]; v.z = ps[p0 + 2]; }
+                if (p0 + 3 < hp) { u.w = pc[p0 + 3]; v.w = ps[p0 + 3]; }
             }
-        }
-    }
-    // SIGN +1: R x, -1: R^T x.  Every lane of the warp takes part.
-    template <int SIGN>
-    __device__ void apply(float (&x)[kVec]) const
-    {
-        if (HALF) {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float o = __shfl_sync(0xffffffffu, x[j], partner);
-                x[j] = fmaf(x[j], c[j % NF], SIGN * s[j % NF] * o);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVec / 2; ++j) {
-                const float u = x[2 * j], v = x[2 * j + 1], sj = SIGN * s[j];
-                x[2 * j] = fmaf(u, c[j], -v * sj);
-                x[2 * j + 1] = fmaf(v, c[j], u * sj);
-            }
+            c.e[0] = c.o[0] = make_float2(u.x, u.y);
+            c.e[1] = c.o[1] = make_float2(u.z, u.w);
+            s.o[0] = make_float2(sign * v.x, sign * v.y);
+            s.o[1] = make_float2(sign * v.z, sign * v.w);
+            s.e[0] = make_float2(-s.o[0].x, -s.o[0].y);
+            s.e[1] = make_float2(-s.o[1].x, -s.o[1].y);
         }
     }
 };
+// The other entries of the pairs.
+template <bool HALF, typename T>
+__device__ __forceinline__ Eight others(const Raw<T> &r, const Eight &x, int partner)
+{
+    if (HALF) return r.from_lane(partner).get();
+    return Eight{{x.o[0], x.o[1]}, {x.e[0], x.e[1]}};
+}
 
 template <int G>
 __device__ __forceinline__ float row_sum(float v)   // over the G lanes of a row
@@ -268,17 +349,11 @@ __device__ __forceinline__ float row_sum(float v)   // over the G lanes of a row
     return v;
 }
 
-__device__ __forceinline__ void load_weight(const float *w, bool on, int l, float (&x)[kVec])
-{
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) x[j] = (w && on) ? w[kVec * l + j] : 1.f;
-}
-
 // Bound by HBM (x read, y written).  G lanes hold a row, 8 entries (16 bytes of bf16) each, so a warp reads 32 / G
-// consecutive heads of a token at once.  A unit is U such reads of one token and side: the rotation factors and the
-// weight are loaded once for all of them, and the U reads are in flight together.
+// consecutive heads of a token at once.  A unit is U such reads of one token and side: the rotation's factors, times
+// the weight, are made once for all of them, and the U reads are in flight together.
 template <typename T, int G, bool HALF, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 qk_norm_rope_k(const __grid_constant__ NormArgs a)
 {
     constexpr int R = 32 / G;
@@ -291,98 +366,106 @@ qk_norm_rope_k(const __grid_constant__ NormArgs a)
     if (side) part -= a.units[0];
     const int H = a.heads[side], h0 = part * U * R + sub;
     const bool in = kVec * l < a.d;
-    const T *x = static_cast<const T *>(a.x[side].p) + token * a.x[side].ld + kVec * l;
-    T *y = static_cast<T *>(a.y[side]) + token * a.ldy[side] + kVec * l;
-    Row8<T> raw[U];
+    const T *x = static_cast<const T *>(a.x[side].p) + token * a.x[side].ld + kVec * l + (size_t)h0 * a.d;
+    T *y = static_cast<T *>(a.y[side]) + token * a.ldy[side] + kVec * l + (size_t)h0 * a.d;
+    Raw<T> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         raw[u].zero();
-        if (in && h0 + u * R < H) raw[u].load(x + (size_t)(h0 + u * R) * a.d);
+        if (in && h0 + u * R < H) raw[u].load(x + u * R * a.d);
     }
-    float w[kVec];
-    load_weight(a.w[side], in, l, w);
-    Turn<HALF> turn;
-    turn.load(a, token, l, lane);
+    const int other = Turn<HALF>::partner(a, l, lane);
+    Turn<HALF> t;
+    t.load(a, token, l, 1.f);
+    const float *w = a.w[side];
+    if (w) {   // the factor of an entry's partner carries the partner's weight
+        const int lp = l + other - lane;
+        const Eight mine = eight_of(w, kVec * l, in, 1.f);
+        const Eight its = HALF ? eight_of(w, kVec * lp, in, 1.f) : Eight{{mine.o[0], mine.o[1]}, {mine.e[0], mine.e[1]}};
+        t.c = times(t.c, mine);
+        t.s = times(t.s, its);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float v[kVec], ss = 0.f;
-        raw[u].get(v);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) ss = fmaf(v[j], v[j], ss);
-        const float r = rsqrtf(fmaf(row_sum<G>(ss), a.inv_d, a.eps));
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = v[j] * r * w[j];
-        turn.template apply<1>(v);
-        if (in && h0 + u * R < H) store8(y + (size_t)(h0 + u * R) * a.d, v);
+        const Eight v = raw[u].get();
+        const float r = rsqrtf(fmaf(row_sum<G>(total(times(v, v))), a.inv_d, a.eps));
+        const Eight o = times(plus_times(v, t.c, times(others<HALF>(raw[u], v, other), t.s)), r);
+        Raw<T> res;
+        res.set(o);
+        if (in && h0 + u * R < H) res.store(y + u * R * a.d);
     }
 }
 
-// Bound by HBM (x and gy read, gx written).  CTAs take one side each and stride over its units, so that the weight's
+// Bound by HBM (x and gy read, gx written).  CTAs take one side each and stride over its visits, so that the weight's
 // gradient gathers in registers; a CTA leaves one [d] partial, and qk_norm_weight_grad_k adds those in a fixed order.
-template <typename T, int G, bool HALF, int U>
-__global__ void __launch_bounds__(kThreads)
+// A visit is a run of `span` units of one token, a unit U reads of 32 / G heads in flight together.  A training batch at
+// d = 64 (252 MB) takes 54 us so, waiting for memory; measured and dropped: the next unit's reads held in registers
+// meanwhile (60 us: it spills), a ring of reads in shared memory per warp (68 us: more instructions).
+template <typename T>
+struct Back {
+    static constexpr int READS = sizeof(T) == 2 ? 5 : 3;   // what 128 registers hold
+};
+
+template <typename T, int G, bool HALF>
+__global__ void __launch_bounds__(kThreads, 2)
 qk_norm_rope_backward_k(const __grid_constant__ NormArgs a)
 {
-    constexpr int R = 32 / G;
+    constexpr int R = 32 / G, U = Back<T>::READS;
     __shared__ float red[kWarps][G * kVec];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, l = lane % G, sub = lane / G;
     const int side = (int)blockIdx.x >= a.ctas[0];
     const int cta = side ? (int)blockIdx.x - a.ctas[0] : (int)blockIdx.x;
-    const int H = a.heads[side], per = a.units[side];
+    const int H = a.heads[side];
     const bool in = kVec * l < a.d;
-    float w[kVec], gw[kVec];
-    load_weight(a.w[side], in, l, w);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) gw[j] = 0.f;
-    const long long units = a.T * per, step = (long long)a.ctas[side] * kWarps;
-    for (long long unit = (long long)cta * kWarps + wid; unit < units; unit += step) {
-        const long long token = (unsigned)unit / (unsigned)per;
-        const int h0 = (int)((unsigned)unit % (unsigned)per) * U * R + sub;
+    const Eight w = eight_of(a.w[side], kVec * l, in, 1.f);
+    Eight gw = zeros();
+    const int other = Turn<HALF>::partner(a, l, lane);
+    const unsigned span = a.span[side], per_token = (a.units[side] + span - 1) / span;
+    const long long visits = a.T * per_token, step = (long long)a.ctas[side] * kWarps;
+    for (long long visit = (long long)cta * kWarps + wid; visit < visits; visit += step) {
+        const unsigned first = (unsigned)visit % per_token * span;
+        const long long token = (unsigned)visit / per_token;
+        Turn<HALF> t;
+        t.load(a, token, l, -1.f);
         const T *x = static_cast<const T *>(a.x[side].p) + token * a.x[side].ld + kVec * l;
         const T *gy = static_cast<const T *>(a.gy[side].p) + token * a.gy[side].ld + kVec * l;
         T *gx = static_cast<T *>(a.y[side]) + token * a.ldy[side] + kVec * l;
-        Row8<T> rx[U], rg[U];
+        const int last = min((int)(first + span) * U * R, H);
+        for (int h0 = (int)first * U * R + sub; h0 - sub < last; h0 += U * R) {
+            Raw<T> rx[U], rg[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            rx[u].zero();
-            rg[u].zero();
-            if (in && h0 + u * R < H) {
-                rx[u].load(x + (size_t)(h0 + u * R) * a.d);
-                rg[u].load(gy + (size_t)(h0 + u * R) * a.d);
+            for (int u = 0; u < U; ++u) {
+                rx[u].zero();
+                rg[u].zero();
+                if (in && h0 + u * R < H) {
+                    rx[u].load(x + (h0 + u * R) * a.d);
+                    rg[u].load(gy + (h0 + u * R) * a.d);
+                }
             }
-        }
-        Turn<HALF> turn;
-        turn.load(a, token, l, lane);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[kVec], m[kVec], ss = 0.f, dot = 0.f;
-            rx[u].get(v);
-            rg[u].get(m);
-            turn.template apply<-1>(m);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                ss = fmaf(v[j], v[j], ss);
-                dot = fmaf(m[j] * w[j], v[j], dot);
+            for (int u = 0; u < U; ++u) {
+                const Eight v = rx[u].get(), g = rg[u].get();
+                const Eight m = plus_times(g, t.c, times(others<HALF>(rg[u], g, other), t.s));
+                const Eight mx = times(m, v), wm = times(m, w);
+                const float ss = row_sum<G>(total(times(v, v))), dot = row_sum<G>(total(times(mx, w)));
+                const bool live = h0 + u * R < H;            // rows past the last head add nothing, whatever eps is
+                const float r = live ? rsqrtf(fmaf(ss, a.inv_d, a.eps)) : 0.f;
+                gw = plus_times(mx, r, gw);
+                const Eight o = times(plus_times(v, -(dot * a.inv_d * r * r), wm), r);
+                Raw<T> res;
+                res.set(o);
+                if (in && live) res.store(gx + (h0 + u * R) * a.d);
             }
-            ss = row_sum<G>(ss);
-            dot = row_sum<G>(dot);
-            const bool live = h0 + u * R < H;            // rows past the last head add nothing, whatever eps is
-            const float r = live ? rsqrtf(fmaf(ss, a.inv_d, a.eps)) : 0.f;
-            const float t = dot * a.inv_d * r * r;
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                gw[j] = fmaf(m[j] * r, v[j], gw[j]);
-                v[j] = r * fmaf(-v[j], t, m[j] * w[j]);
-            }
-            if (in && live) store8(gx + (size_t)(h0 + u * R) * a.d, v);
         }
     }
     if (!a.part) return;
+    const float mine[kVec] = {gw.e[0].x, gw.o[0].x, gw.e[0].y, gw.o[0].y, gw.e[1].x, gw.o[1].x, gw.e[1].y, gw.o[1].y};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
+        float s = mine[j];
 #pragma unroll
-        for (int o = G; o < 32; o <<= 1) gw[j] += __shfl_xor_sync(0xffffffffu, gw[j], o);
-        if (sub == 0) red[wid][kVec * l + j] = gw[j];
+        for (int o = G; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (sub == 0) red[wid][kVec * l + j] = s;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
@@ -393,30 +476,34 @@ qk_norm_rope_backward_k(const __grid_constant__ NormArgs a)
     }
 }
 
-// One block per side and 32 entries of d; its 8 warps each add an eighth of the CTAs' partials, in double.
-__global__ void __launch_bounds__(kThreads)
+// One block per side and 32 entries of d: its 32 warps each add every 32nd of the CTAs' partials, in double.
+constexpr int kSumThreads = 1024;
+constexpr int kBwdCtas = 148 * 2;    // CTAs of the gradient: what is resident at once
+__global__ void __launch_bounds__(kSumThreads)
 qk_norm_weight_grad_k(const float *__restrict__ part, int d, int ctas_q, int ctas_k, float *gwq, float *gwk)
 {
-    __shared__ double red[kWarps][32];
+    constexpr int W = kSumThreads / 32, PER = (kBwdCtas + W - 1) / W;
+    __shared__ double red[W][33];
     const int side = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     float *gw = side ? gwk : gwq;
     if (!gw) return;
     const float *p = part + (side ? (size_t)ctas_q * d : 0);
-    const int n = side ? ctas_k : ctas_q;
+    const int n = side ? ctas_k : ctas_q, at = i < d ? i : d - 1;
+    float v[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) v[k] = wid + k * W < n ? p[(size_t)(wid + k * W) * d + at] : 0.f;
     double s = 0.0;
-    if (i < d)
-        for (int c = wid; c < n; c += kWarps) s += p[(size_t)c * d + i];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) s += v[k];
     red[wid][lane] = s;
     __syncthreads();
-    if (wid == 0 && i < d) {
-#pragma unroll
-        for (int k = 1; k < kWarps; ++k) s += red[k][lane];
-        gw[i] = (float)s;
-    }
+    if (wid != 0) return;
+#pragma unroll 8
+    for (int k = 1; k < W; ++k) s += red[k][lane];
+    if (i < d) gw[i] = (float)s;
 }
 
 // ----------------------------------------------------------------- host
-constexpr int kBwdCtas = 148 * 4;   // resident at once: 4 blocks of 256 threads on each SM
 
 constexpr long long kMaxUnits = 0xfffffff0ll;   // the kernels count units in 32 bits, rounded up to whole blocks
 
@@ -428,33 +515,41 @@ int lanes_per_row(int d)            // the power of two that holds d / 8 lanes
 }
 
 template <typename T, bool HALF, int U>
-void launch_norm(const NormArgs &a, int G, bool back, unsigned grid, cudaStream_t st)
+void launch_norm(const NormArgs &a, int G, unsigned grid, cudaStream_t st)
 {
     switch (G) {
-#define LCLA_G(g)                                                                                  \
-    case g:                                                                                        \
-        if (back) qk_norm_rope_backward_k<T, g, HALF, U><<<grid, kThreads, 0, st>>>(a);            \
-        else qk_norm_rope_k<T, g, HALF, U><<<grid, kThreads, 0, st>>>(a);                          \
-        break;
-        LCLA_G(4) LCLA_G(8) LCLA_G(16) LCLA_G(32)
-#undef LCLA_G
+    case 4: qk_norm_rope_k<T, 4, HALF, U><<<grid, kThreads, 0, st>>>(a); break;
+    case 8: qk_norm_rope_k<T, 8, HALF, U><<<grid, kThreads, 0, st>>>(a); break;
+    case 16: qk_norm_rope_k<T, 16, HALF, U><<<grid, kThreads, 0, st>>>(a); break;
+    default: qk_norm_rope_k<T, 32, HALF, U><<<grid, kThreads, 0, st>>>(a);
+    }
+}
+template <typename T>
+void launch_norm(const NormArgs &a, int G, bool half, int U, unsigned grid, cudaStream_t st)
+{
+    if (half) U == 1 ? launch_norm<T, true, 1>(a, G, grid, st) : launch_norm<T, true, kReads>(a, G, grid, st);
+    else U == 1 ? launch_norm<T, false, 1>(a, G, grid, st) : launch_norm<T, false, kReads>(a, G, grid, st);
+}
+
+template <typename T, bool HALF>
+void launch_norm_backward(const NormArgs &a, int G, unsigned grid, cudaStream_t st)
+{
+    switch (G) {
+    case 4: qk_norm_rope_backward_k<T, 4, HALF><<<grid, kThreads, 0, st>>>(a); break;
+    case 8: qk_norm_rope_backward_k<T, 8, HALF><<<grid, kThreads, 0, st>>>(a); break;
+    case 16: qk_norm_rope_backward_k<T, 16, HALF><<<grid, kThreads, 0, st>>>(a); break;
+    default: qk_norm_rope_backward_k<T, 32, HALF><<<grid, kThreads, 0, st>>>(a);
     }
 }
 
-template <typename T>
-void launch_norm(const NormArgs &a, int G, bool half, int U, bool back, unsigned grid, cudaStream_t st)
-{
-    if (half) U == 1 ? launch_norm<T, true, 1>(a, G, back, grid, st) : launch_norm<T, true, 3>(a, G, back, grid, st);
-    else U == 1 ? launch_norm<T, false, 1>(a, G, back, grid, st) : launch_norm<T, false, 3>(a, G, back, grid, st);
-}
-
-// Units of U reads per token, on each side.  U = 3 keeps three 16-byte reads a lane in flight; a call with too few
-// rows to fill the SMs that way takes U = 1, which has the shorter chain.
+// Units of U reads per token, on each side.  Several 16-byte reads a lane in flight keep HBM busy (480p, 587 MB:
+// 106 us with 3, 100 us with 5, 104 us with 9); a call with too few rows to fill the SMs that way takes U = 1, which
+// has the shorter chain.
 int set_units(NormArgs &a, int G)
 {
     const int R = 32 / G;
     const long long reads = a.T * ((a.heads[0] + R - 1) / R + (a.heads[1] + R - 1) / R);
-    const int U = reads < 148 * 32 ? 1 : 3;
+    const int U = reads < 148 * 32 ? 1 : kReads;
     for (int s = 0; s < 2; ++s) a.units[s] = (a.heads[s] + R * U - 1) / (R * U);
     return U;
 }
@@ -543,6 +638,7 @@ int lcla_rotary_tables(const long long *positions, long long first, int N, int a
             if (!axis_extents || axis_extents[a - 1] < 1) return LCLA_ERR_INVALID_ARG;
             p.extent[a] = axis_extents[a - 1];
         }
+        p.by[a] = make_divisor((unsigned)p.extent[a]);
     }
     if (N > (1 << 30) || first < 0 || first > (1ll << 60)) return LCLA_ERR_UNSUPPORTED;
     if (N == 0) return LCLA_OK;
@@ -556,9 +652,12 @@ int lcla_rotary_tables(const long long *positions, long long first, int N, int a
     p.axes = axes;
     p.N = N;
     p.amp = scaling == LCLA_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
-    const long long threads = ((long long)N * p.pairs + kTabVec - 1) / kTabVec;
-    rotary_tables_k<<<(unsigned)((threads + kTabThreads - 1) / kTabThreads), kTabThreads, 0,
-                      reinterpret_cast<cudaStream_t>(stream)>>>(p, positions, rope_cos, rope_sin);
+    p.narrow = first + N <= 0x7fffffffLL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int vec = p.pairs % 4 == 0 ? 4 : 1, tokens = kTabThreads / (p.pairs / vec) * kTabTokens;
+    const unsigned grid = (unsigned)((N + (long long)tokens - 1) / tokens);
+    if (vec == 4) rotary_tables_k<4><<<grid, kTabThreads, 0, st>>>(p, positions, rope_cos, rope_sin);
+    else rotary_tables_k<1><<<grid, kTabThreads, 0, st>>>(p, positions, rope_cos, rope_sin);
     return launched();
 }
 
@@ -615,8 +714,8 @@ int lcla_qk_norm_rope(const void *q, long long ldq, const void *k, long long ldk
     if (units > kMaxUnits) return LCLA_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)((units + kWarps - 1) / kWarps);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == LCLA_BF16) launch_norm<__nv_bfloat16>(a, G, half_layout != 0, U, false, grid, st);
-    else launch_norm<float>(a, G, half_layout != 0, U, false, grid, st);
+    if (dtype == LCLA_BF16) launch_norm<__nv_bfloat16>(a, G, half_layout != 0, U, grid, st);
+    else launch_norm<float>(a, G, half_layout != 0, U, grid, st);
     return launched();
 }
 
@@ -686,20 +785,28 @@ int lcla_qk_norm_rope_backward(const void *dq_out, long long lddq_out, const voi
     a.eps = eps;
     a.inv_d = 1.f / d;
     if (T > 0) {
-        const int G = lanes_per_row(d), U = set_units(a, G);
-        // the CTAs are dealt out between queries and keys by their units
+        const int G = lanes_per_row(d), R = 32 / G, U = dtype == LCLA_BF16 ? Back<__nv_bfloat16>::READS : Back<float>::READS;
+        for (int s = 0; s < 2; ++s) {
+            a.units[s] = (a.heads[s] + R * U - 1) / (R * U);
+            a.span[s] = T >= kBwdCtas * kWarps && a.units[s] ? a.units[s] : 1;   // whole tokens, if every warp has one
+        }
+        // the CTAs are dealt out between queries and keys by their reads
         const long long uq = T * a.units[0], uk = T * a.units[1];
         if (uq > kMaxUnits || uk > kMaxUnits) return LCLA_ERR_UNSUPPORTED;
-        const long long total = uq + uk, full = (total + kWarps - 1) / kWarps + 1;
+        const long long all = uq + uk, full = (all + kWarps - 1) / kWarps + 1;
         const int ctas = (int)(full < kBwdCtas ? (full < 2 ? 2 : full) : kBwdCtas);
-        a.ctas[1] = uk ? (int)((double)ctas * uk / total) : 0;
+        a.ctas[1] = uk ? (int)((double)ctas * uk / all) : 0;
         if (uk && a.ctas[1] < 1) a.ctas[1] = 1;
         a.ctas[0] = ctas - a.ctas[1];
-        if (dtype == LCLA_BF16) launch_norm<__nv_bfloat16>(a, G, half_layout != 0, U, true, ctas, st);
-        else launch_norm<float>(a, G, half_layout != 0, U, true, ctas, st);
+        const bool half = half_layout != 0;
+        if (dtype == LCLA_BF16)
+            half ? launch_norm_backward<__nv_bfloat16, true>(a, G, ctas, st)
+                 : launch_norm_backward<__nv_bfloat16, false>(a, G, ctas, st);
+        else
+            half ? launch_norm_backward<float, true>(a, G, ctas, st) : launch_norm_backward<float, false>(a, G, ctas, st);
     }
     if (want)
-        qk_norm_weight_grad_k<<<dim3((d + 31) / 32, 2), kThreads, 0, st>>>(static_cast<float *>(workspace), d,
+        qk_norm_weight_grad_k<<<dim3((d + 31) / 32, 2), kSumThreads, 0, st>>>(static_cast<float *>(workspace), d,
                                                                           a.ctas[0], a.ctas[1], dq_weight, dk_weight);
     return launched();
 }
