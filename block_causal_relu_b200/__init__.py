@@ -161,8 +161,13 @@ def plan_segments(B: int, H: int, N: int, d: int, block_len: int, dtype: int) ->
     return [(arr[0][i], arr[1][i], arr[2][i]) for i in range(n)]
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream without its wrapper
+
+
 def _stream(stream, device) -> int:
     if stream is None:
+        if _raw_stream is not None and isinstance(device, int):
+            return _raw_stream(device)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
@@ -357,29 +362,30 @@ def temporal_conv(x: torch.Tensor, tokens_per_frame: int, weight: torch.Tensor,
     return out
 
 
-class _on:
-    """Makes a tensor's device the current one while the library launches on it."""
+def _run(device: int, fn, *args) -> None:
+    """Calls the library with the tensors' device as the current one."""
+    was = torch.cuda.current_device()
+    if was == device:
+        rc = fn(*args)
+    else:
+        torch.cuda.set_device(device)
+        try:
+            rc = fn(*args)
+        finally:
+            torch.cuda.set_device(was)
+    if rc != 0:
+        _check(rc)
 
-    def __init__(self, device: torch.device):
-        self._to, self._was = device.index, torch.cuda.current_device()
 
-    def __enter__(self):
-        if self._to != self._was:
-            torch.cuda.set_device(self._to)
-
-    def __exit__(self, *exc):
-        if self._to != self._was:
-            torch.cuda.set_device(self._was)
-
-
-def _array(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, device) -> None:
-    """A contiguous CUDA tensor of this shape, dtype and device, or None."""
+def _array(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, device: int) -> Optional[int]:
+    """The address of a contiguous CUDA tensor of this shape, dtype and device; None for None."""
     if t is None:
-        return
+        return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{device}")
+    return t.data_ptr()
 
 
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -407,29 +413,28 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
         raise ValueError("negative sizes")
     if positions is None and len(dims) > 1 and (extents is None or len(extents) != len(dims) - 1):
         raise ValueError("extents must hold the sizes of the inner axes")
+    pos = None
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
             raise TypeError("positions must be a CUDA tensor")
-        device = positions.device
-        _array("positions", positions, (n,) if positions.dim() == 1 and len(dims) == 1 else (len(dims), n), torch.int64,
-               device)
+        index = positions.get_device()
+        pos = _array("positions", positions, (n,) if positions.dim() == 1 and len(dims) == 1 else (len(dims), n),
+                     torch.int64, index)
     elif out is not None:
-        device = out[0].device
+        index = out[0].get_device()
     else:
-        device = torch.device(device)
-        if device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
+        index = torch.device(device).index
+        index = torch.cuda.current_device() if index is None else index
     shape = (n, sum(dims) // 2)
-    cos, sin = out if out is not None else (torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2))
-    _array("cos", cos, shape, torch.float32, device)
-    _array("sin", sin, shape, torch.float32, device)
+    if out is None:
+        cos = torch.empty(shape, dtype=torch.float32, device=f"cuda:{index}")
+        out = (cos, torch.empty_like(cos))
+    cos, sin = (_array(name, t, shape, torch.float32, index) for name, t in zip(("cos", "sin"), out))
     ints = ctypes.c_int * 3
-    with _on(device):
-        _check(lib.lcla_rotary_tables(_ptr(positions), int(first), n, len(dims), ints(*dims),
-                                      None if extents is None else ints(*extents), float(theta),
-                                      ROPE_SCALING[scaling], float(factor), float(original_len), float(beta_fast),
-                                      float(beta_slow), _ptr(cos), _ptr(sin), _stream(stream, device)))
-    return cos, sin
+    _run(index, lib.lcla_rotary_tables, pos, int(first), n, len(dims), ints(*dims),
+         None if extents is None else ints(*extents), float(theta), ROPE_SCALING[scaling], float(factor),
+         float(original_len), float(beta_fast), float(beta_slow), cos, sin, _stream(stream, index))
+    return out[0], out[1]
 
 
 def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> int:
@@ -439,38 +444,59 @@ def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> in
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, N, H, d]")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have the shape, dtype and device of its forward tensor")
     B, N, H, d = t.shape
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return H * d
-    if t.stride(3) != 1 and d > 1 or t.stride(2) != d and H > 1:
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 and d > 1 or sh != d and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if N > 1:
-        if B > 1 and t.stride(0) != N * t.stride(1):
+        if B > 1 and sb != N * sn:
             raise ValueError(f"{name}: tokens must be evenly spaced over the batch")
-        return t.stride(1)
-    return t.stride(0) if B > 1 else H * d
+        return sn
+    return sb if B > 1 else H * d
 
 
-def _norm_inputs(q, k, cos, sin, q_weight, k_weight, positions):
+def _norm_call(q, k, cos, sin, q_weight, k_weight, positions, eps, half_layout):
+    """Checks the forward's inputs; what both entry points take of them, and the device."""
     ldq = _rows("q", q)
     B, N, H, d = q.shape
-    code = _dtype_code(q)
-    Hk, ldk = 0, 0
+    code, device = _dtype_code(q), q.get_device()
+    Hk, ldk, kp = 0, 0, None
     if k is not None:
         ldk = _rows("k", k)
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != d or k.dtype != q.dtype or k.device != q.device:
+        Bk, Nk, Hk, dk = k.shape
+        if (Bk, Nk, dk) != (B, N, d) or k.dtype != q.dtype or k.get_device() != device:
             raise ValueError("k must be [B, N, Hk, d] of q's dtype on q's device")
-        Hk = k.shape[2]
+        kp = k.data_ptr()
+    elif k_weight is not None:
+        raise ValueError("k_weight without k")
     if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
         raise ValueError("rope tables must be [rows, rotary_dims / 2]")
-    for name, t in (("cos", cos), ("sin", sin)):
-        _array(name, t, cos.shape, torch.float32, q.device)
-    _array("q_weight", q_weight, (d,), torch.float32, q.device)
-    _array("k_weight", k_weight, (d,), torch.float32, q.device)
-    _array("positions", positions, (B, N), torch.int64, q.device)
-    return B, N, H, Hk, d, code, ldq, ldk
+    rows, pairs = table = cos.shape
+    f32 = torch.float32
+    tail = (B, N, H, Hk, d, _array("q_weight", q_weight, (d,), f32, device),
+            _array("k_weight", k_weight, (d,), f32, device), eps, _array("cos", cos, table, f32, device),
+            _array("sin", sin, table, f32, device), rows, 2 * pairs, 1 if half_layout else 0,
+            _array("positions", positions, (B, N), torch.int64, device))
+    return (q.data_ptr(), ldq, kp, ldk), tail, code, device
+
+
+def _norm_out(q, k, out):
+    """Addresses and distances of the outputs, made unless they are given."""
+    if out is None:
+        form = torch.contiguous_format
+        qo = torch.empty_like(q, memory_format=form)
+        width = q.shape[2] * q.shape[3]
+        if k is None:
+            return (qo, None), (qo.data_ptr(), width, None, 0)
+        ko = torch.empty_like(k, memory_format=form)
+        return (qo, ko), (qo.data_ptr(), width, ko.data_ptr(), k.shape[2] * k.shape[3])
+    qo, ko = out
+    ldk = 0 if k is None else _rows("out k", ko, k)
+    return (qo, ko), (_ptr(qo), _rows("out q", qo, q), None if k is None else _ptr(ko), ldk)
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], rope_cos: torch.Tensor, rope_sin: torch.Tensor, *,
@@ -483,18 +509,10 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], rope_cos: torch.Ten
     2 * rope_cos.shape[1] entries by the table rows at ``positions`` [B, N]
     int64 (token n's own row without).  q and k may be column windows of one
     projection; ``out`` = (q_out, k_out) may be (q, k) themselves."""
-    B, N, H, Hk, d, code, ldq, ldk = _norm_inputs(q, k, rope_cos, rope_sin, q_weight, k_weight, positions)
-    if out is None:
-        out = (torch.empty((B, N, H, d), dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty((B, N, Hk, d), dtype=q.dtype, device=q.device))
-    qo, ko = out
-    with _on(q.device):
-        _check(lib.lcla_qk_norm_rope(
-            _ptr(q), ldq, _ptr(k), ldk, B, N, H, Hk, d, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope_cos),
-            _ptr(rope_sin), rope_cos.shape[0], 2 * rope_cos.shape[1], int(bool(half_layout)), _ptr(positions),
-            _ptr(qo), _rows("out q", qo, q), _ptr(ko), 0 if k is None else _rows("out k", ko, k), code,
-            _stream(stream, q.device)))
-    return qo, ko
+    ins, tail, code, device = _norm_call(q, k, rope_cos, rope_sin, q_weight, k_weight, positions, eps, half_layout)
+    out, to = _norm_out(q, k, out)
+    _run(device, lib.lcla_qk_norm_rope, *ins, *tail, *to, code, _stream(stream, device))
+    return out
 
 
 def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
@@ -506,42 +524,32 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
     """``lcla_qk_norm_rope_backward``: (dq, dk, dq_weight, dk_weight) from the
     gradients of ``qk_norm_rope``'s outputs and its inputs; a weight that was
     not given has no gradient (None)."""
-    B, N, H, Hk, d, code, ldq, ldk = _norm_inputs(q, k, rope_cos, rope_sin, q_weight, k_weight, positions)
-    if k is None and k_weight is not None:
-        raise ValueError("k_weight without k")
-    if out is None:
-        out = (torch.empty((B, N, H, d), dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty((B, N, Hk, d), dtype=q.dtype, device=q.device))
-    dq, dk = out
-    dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
-    need = int(lib.lcla_qk_norm_rope_backward_workspace_bytes(d))
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    with _on(q.device):
-        _check(lib.lcla_qk_norm_rope_backward(
-            _ptr(dq_out), _rows("dq_out", dq_out, q), _ptr(dk_out), 0 if k is None else _rows("dk_out", dk_out, k),
-            _ptr(q), ldq, _ptr(k), ldk, B, N, H, Hk, d, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope_cos),
-            _ptr(rope_sin), rope_cos.shape[0], 2 * rope_cos.shape[1], int(bool(half_layout)), _ptr(positions),
-            _ptr(dq), _rows("out q", dq, q), _ptr(dk), 0 if k is None else _rows("out k", dk, k), _ptr(dqw), _ptr(dkw),
-            code, _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, q.device)))
-    return dq, dk, dqw, dkw
+    ins, tail, code, device = _norm_call(q, k, rope_cos, rope_sin, q_weight, k_weight, positions, eps, half_layout)
+    ldgq = _rows("dq_out", dq_out, q)
+    ldgk = 0 if k is None else _rows("dk_out", dk_out, k)
+    out, to = _norm_out(q, k, out)
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    workspace, size = _workspace(workspace, 0 if dqw is None and dkw is None else
+                                 lib.lcla_qk_norm_rope_backward_workspace_bytes(q.shape[3]), q.device)
+    _run(device, lib.lcla_qk_norm_rope_backward, dq_out.data_ptr(), ldgq, None if k is None else dk_out.data_ptr(),
+         ldgk, *ins, *tail, *to, _ptr(dqw), _ptr(dkw), code, _ptr(workspace), size, _stream(stream, device))
+    return out[0], out[1], dqw, dkw
 
 
 def _gated_inputs(q, k, v, g, scale):
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
+    """(addresses of q, k, v, g), (B, H, N, d, scale), dtype code, device."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
     if q.dim() != 4:
         raise ValueError("q, k, v must share one [B, N, H, d] shape")
-    code = _dtype_code(q)
-    _array("q", q, q.shape, q.dtype, q.device)
-    _array("k", k, q.shape, q.dtype, q.device)
-    _array("v", v, q.shape, q.dtype, q.device)
-    B, N, H, d = q.shape
-    if g is None:
-        raise TypeError("g must be a CUDA tensor")
-    _array("g", g, (B, N, H), torch.float32, q.device)
-    return B, N, H, d, code, float(d ** -0.5 if scale is None else scale)
+    if g is None or k is None or v is None:
+        raise TypeError("k, v and g must be CUDA tensors")
+    shape, dtype, device = q.shape, q.dtype, q.get_device()
+    B, N, H, d = shape
+    ptrs = (_array("q", q, shape, dtype, device), _array("k", k, shape, dtype, device),
+            _array("v", v, shape, dtype, device), _array("g", g, (B, N, H), torch.float32, device))
+    return ptrs, (B, H, N, d, float(d ** -0.5 if scale is None else scale)), _dtype_code(q), device
 
 
 def _workspace(workspace, need: int, device):
@@ -567,19 +575,19 @@ def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     scale S_t q_t over q, k, v [B, N, H, d] with log decays g [B, N, H] fp32 and
     scale d^-1/2 unless given.  Returns (out, state after the last token
     [B, H, d, d] fp32 or None)."""
-    B, N, H, d, code, scale = _gated_inputs(q, k, v, g, scale)
+    ptrs, dims, code, device = _gated_inputs(q, k, v, g, scale)
+    B, H, N, d, _ = dims
     st = (B, H, d, d)
-    _array("state_in", state_in, st, torch.float32, q.device)
+    s0 = _array("state_in", state_in, st, torch.float32, device)
     if out is None:
         out = torch.empty_like(q)
     if state_out is None and want_state:
         state_out = torch.empty(st, dtype=torch.float32, device=q.device)
-    _array("out", out, q.shape, q.dtype, q.device)
-    _array("state_out", state_out, st, torch.float32, q.device)
-    workspace, size = _workspace(workspace, gated_forward_workspace_bytes(B, H, N, d, code), q.device)
-    with _on(q.device):
-        _check(lib.lcla_gated_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), B, H, N, d, scale, _ptr(state_in), _ptr(out),
-                                      _ptr(state_out), code, _ptr(workspace), size, _stream(stream, q.device)))
+    op = _array("out", out, q.shape, q.dtype, device)
+    s1 = _array("state_out", state_out, st, torch.float32, device)
+    workspace, size = _workspace(workspace, lib.lcla_gated_forward_workspace_bytes(B, H, N, d, code), q.device)
+    _run(device, lib.lcla_gated_forward, *ptrs, *dims, s0, op, s1, code, _ptr(workspace), size,
+         _stream(stream, device))
     return out, state_out
 
 
@@ -595,15 +603,15 @@ def gated_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     if state_out is not None:
         return gated_forward(q, k, v, g, scale, state_in=state, out=out, state_out=state_out if save else None,
                              want_state=False, workspace=workspace, stream=stream)[0]
-    B, L, H, d, code, scale = _gated_inputs(q, k, v, g, scale)
-    _array("state", state, (B, H, d, d), torch.float32, q.device)
+    ptrs, dims, code, device = _gated_inputs(q, k, v, g, scale)
+    B, H, L, d, _ = dims
+    sp = _array("state", state, (B, H, d, d), torch.float32, device)
     if out is None:
         out = torch.empty_like(q)
-    _array("out", out, q.shape, q.dtype, q.device)
-    workspace, size = _workspace(workspace, gated_forward_workspace_bytes(B, H, L, d, code), q.device)
-    with _on(q.device):
-        _check(lib.lcla_gated_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), B, H, L, d, scale, _ptr(state), int(bool(save)),
-                                   _ptr(out), code, _ptr(workspace), size, _stream(stream, q.device)))
+    op = _array("out", out, q.shape, q.dtype, device)
+    workspace, size = _workspace(workspace, lib.lcla_gated_forward_workspace_bytes(B, H, L, d, code), q.device)
+    _run(device, lib.lcla_gated_step, *ptrs, *dims, sp, 1 if save else 0, op, code, _ptr(workspace), size,
+         _stream(stream, device))
     return out
 
 
@@ -615,21 +623,20 @@ def gated_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     """``lcla_gated_backward``: (dq, dk, dv, dg, dstate_in or None) from the
     gradients of ``gated_forward``'s outputs and its inputs; ``out`` gives the
     buffers of the first four."""
-    B, N, H, d, code, scale = _gated_inputs(q, k, v, g, scale)
-    if not isinstance(dout, torch.Tensor):
+    ptrs, dims, code, device = _gated_inputs(q, k, v, g, scale)
+    B, H, N, d, _ = dims
+    if dout is None:
         raise TypeError("dout must be a CUDA tensor")
-    _array("dout", dout, q.shape, q.dtype, q.device)
-    st = (B, H, d, d)
-    _array("state_in", state_in, st, torch.float32, q.device)
-    _array("dstate_out", dstate_out, st, torch.float32, q.device)
-    dq, dk, dv, dg = out if out is not None else (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q),
-                                                 torch.empty_like(g))
-    for name, t, like in (("dq", dq, q), ("dk", dk, q), ("dv", dv, q), ("dg", dg, g)):
-        _array(name, t, like.shape, like.dtype, q.device)
-    ds = torch.empty(st, dtype=torch.float32, device=q.device) if want_dstate_in else None
-    workspace, size = _workspace(workspace, gated_backward_workspace_bytes(B, H, N, d, code), q.device)
-    with _on(q.device):
-        _check(lib.lcla_gated_backward(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(g), B, H, N, d, scale,
-                                       _ptr(state_in), _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-                                       _ptr(ds), code, _ptr(workspace), size, _stream(stream, q.device)))
-    return dq, dk, dv, dg, ds
+    dp = _array("dout", dout, q.shape, q.dtype, device)
+    st, f32 = (B, H, d, d), torch.float32
+    s0 = _array("state_in", state_in, st, f32, device)
+    ds1 = _array("dstate_out", dstate_out, st, f32, device)
+    if out is None:
+        out = (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q), torch.empty_like(g))
+    to = [_array(name, t, like.shape, like.dtype, device)
+          for name, t, like in zip(("dq", "dk", "dv", "dg"), out, (q, q, q, g))]
+    ds0 = torch.empty(st, dtype=f32, device=q.device) if want_dstate_in else None
+    workspace, size = _workspace(workspace, lib.lcla_gated_backward_workspace_bytes(B, H, N, d, code), q.device)
+    _run(device, lib.lcla_gated_backward, dp, *ptrs, *dims, s0, ds1, *to, _ptr(ds0), code, _ptr(workspace), size,
+         _stream(stream, device))
+    return (*out, ds0)
