@@ -151,49 +151,69 @@ struct Scan {
     int nseg, BH, n4;          // n4: float4s of a state
 };
 
-// One thread per float4 of a state; the segments' values are read 16 at a time ahead of the chain.
-__global__ void __launch_bounds__(128) gated_scan_k(const __grid_constant__ Scan s)
+// One lane per float4 of a state, the segments dealt out in runs of SCAN_RUN over the block's warps.  Bound by latency:
+// a warp reads its run at once, the runs' sums and decays meet in shared memory, and each warp then carries the state
+// through its run (47 segments at d = 64: 9.4 us with one thread for all of them, 8 read ahead of the chain).
+constexpr int SCAN_WARPS = 8, SCAN_RUN = 8;      // warps at most: as many as there are runs
+__device__ __forceinline__ float4 decayed_plus(const float4 &c, float d, const float4 &v)
 {
+    return make_float4(fmaf(c.x, d, v.x), fmaf(c.y, d, v.y), fmaf(c.z, d, v.z), fmaf(c.w, d, v.w));
+}
+__global__ void __launch_bounds__(SCAN_WARPS * 32) gated_scan_k(const __grid_constant__ Scan s)
+{
+    __shared__ float4 sums[SCAN_WARPS][32];
+    __shared__ float decays[SCAN_WARPS][32];
     after_launch_before();
-    const int i = blockIdx.x * 128 + threadIdx.x, dir = blockIdx.y;
-    const int all = s.BH * s.n4;
-    if (i >= all) return;
-    const int bh = i / s.n4;
-    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, dir = blockIdx.y;
+    const int i = blockIdx.x * 32 + lane, all = s.BH * s.n4, bh = i / s.n4;      // n4 is a multiple of 32
+    float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
     if (s.init[dir]) {
-        c = reinterpret_cast<const float4 *>(s.init[dir])[i];
+        const float4 c = reinterpret_cast<const float4 *>(s.init[dir])[i];
         const float m = s.init_scale[dir];
-        c.x *= m; c.y *= m; c.z *= m; c.w *= m;
+        carry = make_float4(c.x * m, c.y * m, c.z * m, c.w * m);
     }
     float4 *part = reinterpret_cast<float4 *>(s.part[dir]);
-    constexpr int U = 16;
-    for (int k0 = 0; k0 < s.nseg; k0 += U) {
-        float4 v[U];
-        float d[U];
+    auto at = [&](int k) { return dir ? s.nseg - 1 - k : k; };
+    for (int first = 0; first < s.nseg; first += warps * SCAN_RUN) {
+        const int k0 = first + warp * SCAN_RUN;
+        float4 v[SCAN_RUN];
+        float d[SCAN_RUN];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = dir ? s.nseg - 1 - (k0 + u) : k0 + u;
+        for (int u = 0; u < SCAN_RUN; ++u) {            // loads without branches go out together
+            const int k = at(min(k0 + u, s.nseg - 1));
+            v[u] = part[(size_t)k * all + i];
+            d[u] = s.decays[(size_t)k * s.BH + bh];
+        }
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float decay = 1.f;
+#pragma unroll
+        for (int u = 0; u < SCAN_RUN; ++u)
             if (k0 + u < s.nseg) {
-                v[u] = part[(size_t)k * all + i];
-                d[u] = s.decays[(size_t)k * s.BH + bh];
+                sum = decayed_plus(sum, d[u], v[u]);
+                decay *= d[u];
             }
+        sums[warp][lane] = sum;
+        decays[warp][lane] = decay;
+        __syncthreads();
+        float4 c = carry;
+#pragma unroll
+        for (int w = 0; w < SCAN_WARPS; ++w) {
+            if (w == warp) c = carry;
+            if (w < warps) carry = decayed_plus(carry, decays[w][lane], sums[w][lane]);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = dir ? s.nseg - 1 - (k0 + u) : k0 + u;
+        for (int u = 0; u < SCAN_RUN; ++u)
             if (k0 + u < s.nseg) {
-                part[(size_t)k * all + i] = c;
-                c.x = fmaf(c.x, d[u], v[u].x);
-                c.y = fmaf(c.y, d[u], v[u].y);
-                c.z = fmaf(c.z, d[u], v[u].z);
-                c.w = fmaf(c.w, d[u], v[u].w);
+                part[(size_t)at(k0 + u) * all + i] = c;
+                c = decayed_plus(c, d[u], v[u]);
             }
-        }
+        __syncthreads();                                // the sums have been read
     }
-    if (s.last2[dir]) reinterpret_cast<float4 *>(s.last2[dir])[i] = c;
+    if (warp != 0) return;
+    if (s.last2[dir]) reinterpret_cast<float4 *>(s.last2[dir])[i] = carry;
     if (s.last[dir]) {
         const float m = s.last_scale[dir];
-        reinterpret_cast<float4 *>(s.last[dir])[i] = make_float4(c.x * m, c.y * m, c.z * m, c.w * m);
+        reinterpret_cast<float4 *>(s.last[dir])[i] = make_float4(carry.x * m, carry.y * m, carry.z * m, carry.w * m);
     }
 }
 
@@ -328,42 +348,60 @@ struct Plan {
     size_t before, after, decays, dot, bytes;   // workspace offsets
 };
 
-template <int D>
-int slots(int dtype)
+// Microseconds of a tile step of the forward's recurrence with one block on an SM, whose warps wait for one instruction
+// after another, and with as many as fit, which keep the matrix units and issue slots busy.
+struct StepTime {
+    double one, full;
+    int blocks;
+};
+StepTime step_time(int d, int dtype)
 {
-    return kSms * (dtype == LCLA_BF16 ? Shape<__nv_bfloat16, D>::BLOCKS : Shape<float, D>::BLOCKS);
+    if (dtype == LCLA_BF16)
+        return d == 32 ? StepTime{1.3, 3.0, Shape<__nv_bfloat16, 32>::BLOCKS} : StepTime{1.9, 3.0, Shape<__nv_bfloat16, 64>::BLOCKS};
+    return d == 32 ? StepTime{3.0, 4.6, Shape<float, 32>::BLOCKS} : StepTime{7.0, 8.6, Shape<float, 64>::BLOCKS};
 }
 
-// How many segments: the time of a tile step of all blocks on an SM grows with them once they hide its latency, so
-// the candidates are those that fill whole rounds of resident blocks; more segments than one cost the totals and the
-// scan.  All in microseconds, measured (constants below).
+// A kernel of n blocks over segments of ts tiles; each block spends about 1.5 steps on its start and end.
+double kernel_time(long long n, long long ts, const StepTime &t)
+{
+    const long long cap = (long long)kSms * t.blocks, rounds = n / cap, rest = n % cap;
+    double steps = rounds * t.full;
+    if (rest) steps += t.one + (t.full - t.one) * ((rest + kSms - 1) / kSms - 1) / (t.blocks - 1);
+    return steps * (ts + 1.5);
+}
+
+// How many segments: the cheapest by this estimate, which was within 10 % of what was measured over 1 to 147 tiles and
+// 1 to 49 segments (bf16, d = 64 gradient of 2 x 35 heads: 147 tiles in 8 segments 304 us estimated, 310 measured; 10
+// tiles in 1 and 4 segments 73 and 43, 75 and 46).  A step of the totals costs half of the forward's, one of dq and dk
+// 1.4 times; the scan and the launches 6 us and more with each segment.
 Plan make_plan(int B, int H, int N, int d, int dtype, bool backward)
 {
     Plan p = {};
     if (N == 0 || (!backward && N <= kShort)) return p;
     const int tiles = (N + TILE - 1) / TILE, ns = d / 32, G = WARPS / ns;
-    const long long per_seg = (long long)((H + G - 1) / G) * B * (backward ? 2 : 1);
-    const long long cap = d == 32 ? slots<32>(dtype) : slots<64>(dtype);
-    const double alone = 1.0, full = 2.2, fixed = 8.0;      // a tile step on an empty and a full SM; totals and scan
+    const long long per_seg = (long long)((H + G - 1) / G) * B;
+    const StepTime t = step_time(d, dtype);
     double best = 1e30;
     p.nseg = 1;
     p.seg_tiles = tiles;
-    for (int c = 0; c <= 16; ++c) {
-        long long nseg = c == 0 ? 1 : c * cap / per_seg;
-        if (nseg < 1 || (c && nseg == 1)) continue;
-        if (nseg > tiles) nseg = tiles;
-        long long ts = (tiles + nseg - 1) / nseg;
-        if (backward && ts > kGateTiles) ts = kGateTiles;
-        nseg = (tiles + ts - 1) / ts;
-        const long long blocks = nseg * per_seg, rounds = (blocks + cap - 1) / cap;
-        const double share = blocks >= cap ? 1.0 : (double)blocks / cap;
-        const double step = full * share > alone ? full * share : alone;
-        const double cost = rounds * (ts + 1.5) * step * (nseg > 1 ? 1.45 : 1.0) + (nseg > 1 ? fixed : 0.0);
+    auto consider = [&](long long ts) {
+        if (ts < 1 || ts > tiles || (backward && ts > kGateTiles)) return;
+        const long long nseg = (tiles + ts - 1) / ts, b = nseg * per_seg;
+        double cost = kernel_time(b, ts, t);
+        if (backward) cost += 1.4 * kernel_time(2 * b, ts, t) + 0.5 * kernel_time(2 * b, ts, t) + 4.0;
+        else if (nseg > 1) cost += 0.5 * kernel_time(b, ts, t);
+        if (backward || nseg > 1) cost += 6.0 + 0.08 * nseg;
         if (cost < best) {
             best = cost;
             p.nseg = (int)nseg;
             p.seg_tiles = (int)ts;
         }
+    };
+    consider(tiles);
+    for (long long ts = 1; ts <= 64; ++ts) consider(ts);
+    for (long long c = 1; c <= 16; ++c) {       // segments that fill c rounds of resident blocks
+        const long long nseg = c * kSms * t.blocks / per_seg;
+        if (nseg > 1) consider((tiles + nseg - 1) / nseg);
     }
     const size_t slice = (size_t)B * H * d * d * sizeof(float);
     size_t at = 0;
@@ -436,7 +474,8 @@ void launch_totals(const Work &w, const Totals &t, int roles, cudaStream_t st)
 
 void launch_scan(const Scan &s, int dirs, cudaStream_t st)
 {
-    launch_after(gated_scan_k, dim3((s.BH * s.n4 + 127) / 128, dirs), 128, 0, st, s);
+    const int runs = (s.nseg + SCAN_RUN - 1) / SCAN_RUN;
+    launch_after(gated_scan_k, dim3(s.BH * (s.n4 / 32), dirs), 32 * (runs < SCAN_WARPS ? runs : SCAN_WARPS), 0, st, s);
 }
 
 template <typename T, int D>
