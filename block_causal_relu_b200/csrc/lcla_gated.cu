@@ -312,7 +312,7 @@ gated_short_k(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     for (int t = 0; t < N; ++t) {
         const size_t tok = (size_t)b * N + t, row = (tok * H + h) * D;
         const float gt = g[tok * H + h];
-        const float a = expf(gt < RESET ? RESET : gt);
+        const float a = expf(bounded(gt));
         float kk[4], qq[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

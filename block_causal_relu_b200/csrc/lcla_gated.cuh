@@ -40,7 +40,7 @@ namespace gated {
 constexpr int TILE = 32;           // tokens per tile
 constexpr int WARPS = 4;           // warps per block: 4 heads at d = 32, 2 at d = 64
 constexpr int THREADS = WARPS * 32;
-constexpr float RESET = -1000.f;   // a log decay below this counts as this: e^-1000 is zero in fp32
+constexpr float RESET = -1000.f;   // a log decay below this counts as this: e^-1000 is zero in fp32, e^1000 infinite
 
 // ---------------------------------------------------------------- operands
 // A pair is two neighbouring entries of the contraction index in one lane.  In<T> holds them as given: one bf16x2
@@ -339,29 +339,52 @@ struct Weights {
     float out[TILE];         // weight of each token in the next state
 };
 
-// Reads one log decay per lane; returns the decay of the whole tile and, in `total`, its G / ln 2.
+__device__ __forceinline__ float bounded(float g) { return g < RESET ? RESET : g > -RESET ? -RESET : g; }
+
+// Nearest whole number and the rest of |x| < 2^31, by adding 1.5 * 2^52 to it.
+__device__ __forceinline__ void whole_and_rest(double x, float &whole, float &rest)
+{
+    const double t = x + 6755399441055744.0;
+    whole = (float)__double2loint(t);
+    rest = (float)(x - (t - 6755399441055744.0));
+}
+
+// 2^(whole + rest), |rest| <= 1/2, within an fp32 rounding or two: the Taylor polynomial of degree 7 of 2^rest, whose
+// remainder (ln 2 / 2)^8 / 8! is 5e-9, times an exact power.  A state of many tiles ago has been multiplied by as many
+// decays: the 2^-22 of the approximate instruction would add up (measured: 1e-6 of the state over 145 segments).
+__device__ __forceinline__ float exact_ex2(float whole, float rest)
+{
+    float p = 1.5252734e-5f;
+    p = fmaf(p, rest, 1.5403530e-4f);
+    p = fmaf(p, rest, 1.3333558e-3f);
+    p = fmaf(p, rest, 9.6181291e-3f);
+    p = fmaf(p, rest, 5.5504109e-2f);
+    p = fmaf(p, rest, 2.4022651e-1f);
+    p = fmaf(p, rest, 6.9314718e-1f);
+    return fmaf(p, rest, 1.f) * ex2(whole);
+}
+
+// Reads one log decay per lane; returns the decay of the whole tile and, in lane 31's `total`, its G / ln 2.
 __device__ __forceinline__ float tile_weights(Weights *w, float g, bool rev, int lane, double &total)
 {
-    double G = (double)(g < RESET ? RESET : g) * 1.4426950408889634;
+    double G = (double)bounded(g) * 1.4426950408889634;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const double up = __shfl_up_sync(0xffffffffu, G, o);
         if (lane >= o) G += up;
     }
-    const double end = __shfl_sync(0xffffffffu, G, 31);
-    const double whole = floor(G);
-    const float a = (float)whole, b = (float)(G - whole);
-    const float fromstart = ex2((float)G), toend = ex2((float)(end - G));
+    total = G;
+    float a, b;
+    whole_and_rest(G, a, b);
+    const float ea = __shfl_sync(0xffffffffu, a, 31), eb = __shfl_sync(0xffffffffu, b, 31);
+    const float fromstart = ex2(a + b), toend = ex2((ea - a) + (eb - b));
     __syncwarp();                          // the previous tile's weights have been read
     w->whole[lane] = rev ? a : -a;
     w->frac[lane] = rev ? b : -b;
     w->in[lane] = rev ? toend : fromstart;
     w->out[lane] = rev ? fromstart : toend;
     __syncwarp();
-    total = end;
-    // A state of many tiles ago has been multiplied by as many decays: the approximation's error of 2^-22 each would
-    // add up (measured: 1e-6 of the state over 145 segments), so these are rounded once from double.
-    return (float)exp2(end);
+    return exact_ex2(ea, eb);
 }
 
 template <int NS>
@@ -761,7 +784,7 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
     wait_copies<0>();
     const size_t at_s = ((size_t)seg * w.B + b) * w.H + h;
     write_state<D>(S, part + at_s * D * D, slab, lane);
-    if (decays && slab == 0 && lane == 0) decays[at_s] = (float)exp2(sum);
+    if (decays && slab == 0 && lane == 31) decays[at_s] = (float)exp2(sum);
 }
 
 }  // namespace gated
