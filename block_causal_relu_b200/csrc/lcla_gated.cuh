@@ -425,58 +425,67 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
+// The warp's 32 values of all tokens of a tile, transposed: [16-token block][16-value block][half][token half].  `flip`
+// exchanges the token blocks, so that a direction known only at run time needs no register chosen at run time.
+template <typename T>
+using Values = In<T>[2][2][2][2];
+template <typename T, int D>
+__device__ __forceinline__ void load_values(Values<T> &v, uint32_t vt, bool flip, int slab, int lane)
+{
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) load_t<D>(v[sb][m], vt, flip ? 1 - sb : sb, 2 * slab + m, lane);
+}
+
 // S <- decay S + sum over the tile's tokens of (weight v) k^T, for the warp's 32 values and all keys.  Each tile's
 // sum starts from zero and meets the state in one rounded multiply-add: the matrix units cut off low bits as they
 // accumulate, which a long sum in them would collect.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, uint32_t vt, const Weights *w, int slab,
-                                       float decay, int lane)
+__device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, const Values<T> &v, bool flip,
+                                       const Weights *w, float decay, int lane)
 {
+    Co<T, NT> a[2][2][4];                                // [value block][token block]
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        Co<T, NT> a[2][4];
+    for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-            In<T> v[2][2];
-            load_t<D>(v, vt, sb, 2 * slab + m, lane);
+        for (int kh = 0; kh < 2; ++kh) {
+            const int row = 16 * (flip ? 1 - sb : sb) + 8 * kh + 2 * (lane & 3);
+            const float2 u = *reinterpret_cast<const float2 *>(&w->out[row]);
 #pragma unroll
-            for (int kh = 0; kh < 2; ++kh) {
-                const float2 u = *reinterpret_cast<const float2 *>(&w->out[16 * sb + 8 * kh + 2 * (lane & 3)]);
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int fh = 0; fh < 2; ++fh) {
-                    split(a[sb][2 * kh + fh], mul2(value(v[fh][kh]), u));
-                }
-            }
+                for (int fh = 0; fh < 2; ++fh) split(a[m][sb][2 * kh + fh], mul2(value(v[sb][m][fh][kh]), u));
         }
 #pragma unroll
-        for (int e0 = 0; e0 < D / 16; e0 += 2) {         // 32 keys: four sums side by side
-            In<T> k[2][2][2][2];
-            float c[4][4];
+    for (int e = 0; e < D / 16; ++e) {                   // 16 keys: four sums side by side
+        In<T> k[2][2][2];
+        float c[2][2][4];
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb)
+        for (int sb = 0; sb < 2; ++sb) load_t<D>(k[sb], kt, flip ? 1 - sb : sb, e, lane);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) load_t<D>(k[sb][e], kt, sb, e0 + e, lane);
+        for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb)
+            for (int i = 0; i < Steps<T, NT>::N; ++i)
 #pragma unroll
-                for (int i = 0; i < Steps<T, NT>::N; ++i)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const In<T>(&kk)[2] = k[sb][n >> 1][n & 1];
-                        if (sb == 0 && i == 0) mma<true>(i, c[n], a[sb], kk[0], kk[1]);
-                        else mma<false>(i, c[n], a[sb], kk[0], kk[1]);
+                    for (int n = 0; n < 2; ++n) {
+                        if (sb == 0 && i == 0) mma<true>(i, c[m][n], a[m][sb], k[sb][n][0], k[sb][n][1]);
+                        else mma<false>(i, c[m][n], a[m][sb], k[sb][n][0], k[sb][n][1]);
                     }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                float(&st)[4] = S[m][2 * e0 + n];
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float(&st)[4] = S[m][2 * e + n];
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
-                    const float2 r = fma2(make_float2(st[i], st[i + 1]), both(decay), make_float2(c[n][i], c[n][i + 1]));
+                    const float2 r = fma2(make_float2(st[i], st[i + 1]), both(decay), make_float2(c[m][n][i], c[m][n][i + 1]));
                     st[i] = r.x;
                     st[i + 1] = r.y;
                 }
             }
-        }
     }
 }
 
@@ -612,11 +621,11 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
         auto block = [&](int m) { return rev ? 1 - m : m; };
         // the carried state's part of the outputs
         float acc[2][4][4];
+        In<T> q[2][D / 16][4];
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-            In<T> a[2][4];
-            load_a<D>(a[0], qt, block(0), ks, lane);
-            load_a<D>(a[1], qt, block(1), ks, lane);
+            load_a<D>(q[0][ks], qt, block(0), ks, lane);
+            load_a<D>(q[1][ks], qt, block(1), ks, lane);
             Co<T, NQ> s[4][2];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -631,11 +640,13 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        if (ks == 0 && j == 0) mma<true>(j, acc[m][c], a[m], s[c][0], s[c][1]);
-                        else mma<false>(j, acc[m][c], a[m], s[c][0], s[c][1]);
+                        if (ks == 0 && j == 0) mma<true>(j, acc[m][c], q[m][ks], s[c][0], s[c][1]);
+                        else mma<false>(j, acc[m][c], q[m][ks], s[c][0], s[c][1]);
                     }
         }
         // the tile's own part
+        Values<T> v;
+        load_values<T, D>(v, vt, rev, slab, lane);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int row0 = 16 * block(m);
@@ -659,15 +670,14 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                 float sc[2][4];
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    In<T> a[4], k[2][2];
-                    load_a<D>(a, qt, block(m), ks, lane);
+                    In<T> k[2][2];
                     load_b<D>(k, kt, sb, ks, lane);
 #pragma unroll
                     for (int i = 0; i < Steps<T, 1>::N; ++i)
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt) {
-                            if (ks == 0 && i == 0) mma<true>(i, sc[nt], a, k[nt][0], k[nt][1]);
-                            else mma<false>(i, sc[nt], a, k[nt][0], k[nt][1]);
+                            if (ks == 0 && i == 0) mma<true>(i, sc[nt], q[m][ks], k[nt][0], k[nt][1]);
+                            else mma<false>(i, sc[nt], q[m][ks], k[nt][0], k[nt][1]);
                         }
                 }
                 Co<T, NP> p[4];
@@ -688,13 +698,10 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                         split(p[2 * nt + hh], x);
                     }
                 }
-                In<T> v[2][2][2];
-#pragma unroll
-                for (int cb = 0; cb < 2; ++cb) load_t<D>(v[cb], vt, sb, 2 * slab + cb, lane);
 #pragma unroll
                 for (int i = 0; i < Steps<T, NP>::N; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mma<false>(i, acc[m][c], p, v[c >> 1][c & 1][0], v[c >> 1][c & 1][1]);
+                    for (int c = 0; c < 4; ++c) mma<false>(i, acc[m][c], p, v[j][c >> 1][c & 1][0], v[j][c >> 1][c & 1][1]);
             }
             const int t = t0 + row0 + (lane >> 2);
 #pragma unroll
@@ -731,7 +738,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
             }
             write_rows<T>(out + (size_t)t * row, row, acc[m], t, w.N, lane);
         }
-        if (i + 1 < n || r.state_end) update<T, D, NU>(S, kt, vt, wt, slab, decay, lane);
+        if (i + 1 < n || r.state_end) update<T, D, NU>(S, kt, v, rev, wt, decay, lane);
     }
     wait_copies<0>();
     if (r.state_end) write_state<D>(S, r.state_end + ((size_t)b * w.H + h) * D * D, slab, lane);
@@ -779,7 +786,9 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
         group_sync<NS>(group);
         load(i + STAGES - 1);
         const uint32_t kt = ring + (i % STAGES) * STAGE;
-        update<T, D, NT>(S, kt, kt + L::BYTES, wt, slab, decay, lane);
+        Values<T> v;
+        load_values<T, D>(v, kt + L::BYTES, false, slab, lane);
+        update<T, D, NT>(S, kt, v, false, wt, decay, lane);
     }
     wait_copies<0>();
     const size_t at_s = ((size_t)seg * w.B + b) * w.H + h;
