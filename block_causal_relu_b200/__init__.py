@@ -4,7 +4,9 @@ Thin binding of the C-ABI library ``liblcla.so`` (declared in
 ``include/lcla.h``): it checks and marshals torch tensors (device memory and
 the current CUDA stream) into its entry points -- the whole-sequence forward
 (uniform or explicit blocks), the streaming step, the two halves of a
-sequence-sharded forward and the Mix-FFN temporal convolution.  Every step of
+sequence-sharded forward, the Mix-FFN temporal convolution, and the gated
+linear attention operators: rotary tables, the per-head norm of q and k with the
+rotation, and the gated recurrence with its step and gradients.  Every step of
 the computation runs in the library's sm_100a kernels; there is no other path.
 Importing this package fails if the library has not been built
 (``python block_causal_relu_b200/build.py``).
@@ -20,7 +22,8 @@ import torch
 __all__ = ["forward", "step", "forward_workspace_bytes", "step_workspace_bytes", "plan_info",
            "forward_blocks", "forward_blocks_workspace_bytes", "temporal_conv",
            "rotary_tables", "qk_norm_rope", "qk_norm_rope_backward",
-           "gated_forward", "gated_step", "gated_backward",
+           "gated_forward", "gated_step", "gated_backward", "gated_forward_workspace_bytes",
+           "gated_backward_workspace_bytes",
            "shard_begin", "shard_end", "shard_workspace_bytes", "device_status", "selftest_bounded_wait",
            "LclaError", "LIB_PATH", "lib", "BF16", "F32", "D", "HEAD_DIMS"]
 
@@ -388,6 +391,18 @@ def _array(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtyp
     return t.data_ptr()
 
 
+def _hold(stream, device: int, *tensors) -> None:
+    """Memory made here on the current stream for work on another one is not
+    given out again before that work has run."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -434,6 +449,7 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     _run(index, lib.lcla_rotary_tables, pos, int(first), n, len(dims), ints(*dims),
          None if extents is None else ints(*extents), float(theta), ROPE_SCALING[scaling], float(factor),
          float(original_len), float(beta_fast), float(beta_slow), cos, sin, _stream(stream, index))
+    _hold(stream, index, *out)
     return out[0], out[1]
 
 
@@ -512,6 +528,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], rope_cos: torch.Ten
     ins, tail, code, device = _norm_call(q, k, rope_cos, rope_sin, q_weight, k_weight, positions, eps, half_layout)
     out, to = _norm_out(q, k, out)
     _run(device, lib.lcla_qk_norm_rope, *ins, *tail, *to, code, _stream(stream, device))
+    _hold(stream, device, *out)
     return out
 
 
@@ -534,6 +551,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
                                  lib.lcla_qk_norm_rope_backward_workspace_bytes(q.shape[3]), q.device)
     _run(device, lib.lcla_qk_norm_rope_backward, dq_out.data_ptr(), ldgq, None if k is None else dk_out.data_ptr(),
          ldgk, *ins, *tail, *to, _ptr(dqw), _ptr(dkw), code, _ptr(workspace), size, _stream(stream, device))
+    _hold(stream, device, *out, dqw, dkw, workspace)
     return out[0], out[1], dqw, dkw
 
 
@@ -588,6 +606,7 @@ def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     workspace, size = _workspace(workspace, lib.lcla_gated_forward_workspace_bytes(B, H, N, d, code), q.device)
     _run(device, lib.lcla_gated_forward, *ptrs, *dims, s0, op, s1, code, _ptr(workspace), size,
          _stream(stream, device))
+    _hold(stream, device, out, state_out, workspace)
     return out, state_out
 
 
@@ -612,6 +631,7 @@ def gated_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     workspace, size = _workspace(workspace, lib.lcla_gated_forward_workspace_bytes(B, H, L, d, code), q.device)
     _run(device, lib.lcla_gated_step, *ptrs, *dims, sp, 1 if save else 0, op, code, _ptr(workspace), size,
          _stream(stream, device))
+    _hold(stream, device, out, workspace)
     return out
 
 
@@ -639,4 +659,5 @@ def gated_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     workspace, size = _workspace(workspace, lib.lcla_gated_backward_workspace_bytes(B, H, N, d, code), q.device)
     _run(device, lib.lcla_gated_backward, dp, *ptrs, *dims, s0, ds1, *to, _ptr(ds0), code, _ptr(workspace), size,
          _stream(stream, device))
+    _hold(stream, device, *out, ds0, workspace)
     return (*out, ds0)

@@ -279,6 +279,27 @@ def test_graphs_and_streams():
     assert all(torch.equal(a, b) for a, b in zip(eager, sets[0][6]))
 
 
+def test_memory_of_another_stream_is_not_reused():
+    """Calls on a given stream, with memory made and dropped on the current one meanwhile."""
+    q, k, v, g, s0 = make(12, 1, 4000, 6, 32, torch.bfloat16)
+    want = lcla.gated_forward(q, k, v, g, state_in=s0)
+    c, s = lcla.rotary_tables(4000, 32)
+    wantn = lcla.qk_norm_rope(q, k, c, s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        for _ in range(5):
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(2000000)      # the call below waits behind this
+            got = lcla.gated_forward(q, k, v, g, state_in=s0, stream=handle)
+            gotn = lcla.qk_norm_rope(q, k, c, s, stream=handle)
+            lcla.gated_backward(q, q, k, v, g, state_in=s0, stream=handle)      # dropped at once
+            junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 18, 1 << 20, 1 << 22)]
+            side.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((*got, *gotn), (*want, *wantn)))
+            del junk
+
+
 def test_offsets_beyond_32_bits():
     """More than 2^31 elements per tensor: the end of the sequence, from the state before it."""
     H, d, N, tail = 70, 32, 970000, 2051
