@@ -68,9 +68,10 @@ __device__ __forceinline__ void sincos_eighth(long long r, float &s, float &c)
     c = fmaf(y, c, 1.f);
 }
 
-// Bound by its stores once the index arithmetic is out of the way (a first version with divisions and table reads for
-// every four entries took 57 us for the minute-scale latent's 108.6 MB).  A thread keeps VEC entries' frequencies in
-// registers and writes them for kTabTokens tokens; a block covers 256 / (pairs / VEC) tokens at a time.
+// Bound by the integer and conversion instructions it issues, 48 for an entry of both tables: the minute-scale latent's
+// 108.6 MB in 28 us (a first version with divisions and shared-memory reads for every four entries took 57; 32-bit
+// positions and two 32-bit conversions instead of a 64-bit one changed nothing).  A thread keeps VEC entries'
+// frequencies in registers and writes them for kTabTokens tokens; a block covers 256 / (pairs / VEC) tokens at a time.
 template <int VEC>
 __global__ void __launch_bounds__(kTabThreads)
 rotary_tables_k(const __grid_constant__ TabPlan p, const long long *__restrict__ positions, float *__restrict__ cosv,
