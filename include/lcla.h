@@ -383,7 +383,8 @@ LCLA_API int lcla_qk_norm_rope_backward(const void *dq_out, long long lddq_out,
  *   g             [B, N, H] float32 device, 4-byte aligned (so is dg): log
  *                 decays, normally <= 0.  A value
  *                 below -1000, -infinity included, counts as -1000: its e^g is
- *                 zero, which starts a new sequence inside a packed one.
+ *                 zero, which starts a new sequence inside a packed one.  A
+ *                 value above 1000 counts as 1000.
  *   state_in, state_out  [B, H, d, d] float32 device, each may be NULL;
  *                 state_out may be state_in itself.  N = 0 copies the state.
  *   scale         1e-18 <= |scale| <= 1e18.
