@@ -348,9 +348,10 @@ gated_short_k(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 constexpr size_t kAlign = 256;
 size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-// Calls of up to this many tokens take gated_short_k, whose time grows by about 0.4 us a token; the tiles' fixed cost is
-// about 10 us (17 tokens of 59 streams of 8 heads 8.2 us there, one token 5.4 here).
-constexpr int kShort = 16;
+// Calls of a few tokens take gated_short_k, whose time grows with each of them, longer ones the tiles.  Measured in
+// microseconds, tokens by tokens / tiles: bf16, 1 stream x 8 heads, d = 32: 1 token 2.0 / 3.7, 2 2.7 / 3.7, 4 3.9 / 3.7, 8
+// 6.4 / 4.1; 64 x 35, d = 64: 1 10.6 / 23.6, 4 19.9 / 24.0, 8 33.0 / 24.6; fp32, 8 x 35, d = 64: 4 6.3 / 10.0, 8 10.2 / 10.2.
+bool is_short(int N, int dtype) { return N <= (dtype == LCLA_BF16 ? 4 : 8); }
 
 struct Plan {
     int nseg, seg_tiles;
@@ -386,7 +387,7 @@ double kernel_time(long long n, long long ts, const StepTime &t)
 Plan make_plan(int B, int H, int N, int d, int dtype, bool backward)
 {
     Plan p = {};
-    if (N == 0 || (!backward && N <= kShort)) return p;
+    if (N == 0 || (!backward && is_short(N, dtype))) return p;
     const int tiles = (N + TILE - 1) / TILE, ns = d / 32, G = WARPS / ns;
     const long long per_seg = (long long)((H + G - 1) / G) * B;
     const StepTime t = step_time(d, dtype);
@@ -491,7 +492,7 @@ template <typename T, int D>
 int run_forward(const void *q, const void *k, const void *v, const Work &w, const Plan &p, const float *state_in,
                 void *out, float *state_out, unsigned char *ws, cudaStream_t st)
 {
-    if (w.N <= kShort) {
+    if (is_short(w.N, sizeof(T) == 2 ? LCLA_BF16 : LCLA_F32)) {
         gated_short_k<T, D><<<w.B * w.H, THREADS, 0, st>>>((const T *)q, (const T *)k, (const T *)v, w.g, w.H, w.N,
                                                            w.scale, state_in, (T *)out, state_out);
         return launched();

@@ -406,7 +406,7 @@ LCLA_API int lcla_gated_forward(const void *q, const void *k, const void *v, con
  * The same for a block of L tokens (one, when serving) against a carried
  * state, as lcla_step: out uses state and the block; save != 0 leaves the state
  * after the block in `state`, save = 0 leaves it bit-unchanged.  Workspace as
- * lcla_gated_forward with N = L (none for L <= 16).
+ * lcla_gated_forward with N = L (none for L <= 32).
  */
 LCLA_API int lcla_gated_step(const void *q, const void *k, const void *v, const float *g,
                  int B, int H, int L, int d, float scale, float *state, int save,

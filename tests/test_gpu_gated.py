@@ -85,7 +85,8 @@ def within(o, r, A, dtype, bits, what):
 
 
 SHAPES = [  # B, N, H, d, state
-    (1, 1, 1, 32, False), (3, 2, 2, 64, True), (2, 16, 3, 32, True), (1, 17, 1, 64, True), (1, 32, 5, 32, False),
+    (1, 1, 1, 32, False), (3, 2, 2, 64, True), (2, 4, 3, 32, True), (1, 5, 2, 64, True), (2, 8, 1, 64, False),
+    (1, 9, 3, 32, True), (2, 16, 3, 32, True), (1, 17, 1, 64, True), (1, 32, 5, 32, False),
     (2, 33, 4, 32, True), (1, 63, 3, 64, False), (1, 64, 1, 32, True), (2, 257, 5, 64, True), (1, 700, 9, 32, True),
     (1, 1531, 2, 64, False), (1, 2048, 1, 32, True),
 ]
@@ -157,7 +158,7 @@ def test_gradient_against_differences():
 @pytest.mark.parametrize("d", [32, 64])
 def test_stream_of_blocks(d, dtype):
     """Blocks of one to many tokens against the carried state equal one call, and save = 0 leaves the state alone."""
-    B, H, lens = 2, 3, [1, 1, 16, 17, 2, 33, 64, 300, 5]
+    B, H, lens = 2, 3, [1, 1, 16, 17, 2, 33, 64, 300, 5, 4, 9, 8]
     N = sum(lens)
     q, k, v, g, s0 = make(11, B, N, H, d, dtype)
     state = s0.clone()
