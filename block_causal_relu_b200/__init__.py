@@ -444,11 +444,13 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     if out is None:
         cos = torch.empty(shape, dtype=torch.float32, device=f"cuda:{index}")
         out = (cos, torch.empty_like(cos))
-    cos, sin = (_array(name, t, shape, torch.float32, index) for name, t in zip(("cos", "sin"), out))
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        ptrs = [_array(name, t, shape, torch.float32, index) for name, t in zip(("cos", "sin"), out)]
     ints = ctypes.c_int * 3
     _run(index, lib.lcla_rotary_tables, pos, int(first), n, len(dims), ints(*dims),
          None if extents is None else ints(*extents), float(theta), ROPE_SCALING[scaling], float(factor),
-         float(original_len), float(beta_fast), float(beta_slow), cos, sin, _stream(stream, index))
+         float(original_len), float(beta_fast), float(beta_slow), *ptrs, _stream(stream, index))
     _hold(stream, index, *out)
     return out[0], out[1]
 
@@ -576,6 +578,11 @@ def _workspace(workspace, need: int, device):
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
+def _gated_need(B, H, N, d, code) -> int:
+    # a block of one tile (32 tokens) needs none, and a serving step does not ask
+    return 0 if N <= 32 else lib.lcla_gated_forward_workspace_bytes(B, H, N, d, code)
+
+
 def gated_forward_workspace_bytes(B: int, H: int, N: int, d: int, dtype: int) -> int:
     return int(lib.lcla_gated_forward_workspace_bytes(B, H, N, d, dtype))
 
@@ -599,11 +606,15 @@ def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     s0 = _array("state_in", state_in, st, torch.float32, device)
     if out is None:
         out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _array("out", out, q.shape, q.dtype, device)
     if state_out is None and want_state:
         state_out = torch.empty(st, dtype=torch.float32, device=q.device)
-    op = _array("out", out, q.shape, q.dtype, device)
-    s1 = _array("state_out", state_out, st, torch.float32, device)
-    workspace, size = _workspace(workspace, lib.lcla_gated_forward_workspace_bytes(B, H, N, d, code), q.device)
+        s1 = state_out.data_ptr()
+    else:
+        s1 = _array("state_out", state_out, st, torch.float32, device)
+    workspace, size = _workspace(workspace, _gated_need(B, H, N, d, code), q.device)
     _run(device, lib.lcla_gated_forward, *ptrs, *dims, s0, op, s1, code, _ptr(workspace), size,
          _stream(stream, device))
     _hold(stream, device, out, state_out, workspace)
@@ -627,8 +638,10 @@ def gated_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     sp = _array("state", state, (B, H, d, d), torch.float32, device)
     if out is None:
         out = torch.empty_like(q)
-    op = _array("out", out, q.shape, q.dtype, device)
-    workspace, size = _workspace(workspace, lib.lcla_gated_forward_workspace_bytes(B, H, L, d, code), q.device)
+        op = out.data_ptr()
+    else:
+        op = _array("out", out, q.shape, q.dtype, device)
+    workspace, size = _workspace(workspace, _gated_need(B, H, L, d, code), q.device)
     _run(device, lib.lcla_gated_step, *ptrs, *dims, sp, 1 if save else 0, op, code, _ptr(workspace), size,
          _stream(stream, device))
     _hold(stream, device, out, workspace)
@@ -653,8 +666,10 @@ def gated_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     ds1 = _array("dstate_out", dstate_out, st, f32, device)
     if out is None:
         out = (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q), torch.empty_like(g))
-    to = [_array(name, t, like.shape, like.dtype, device)
-          for name, t, like in zip(("dq", "dk", "dv", "dg"), out, (q, q, q, g))]
+        to = [t.data_ptr() for t in out]
+    else:
+        to = [_array(name, t, like.shape, like.dtype, device)
+              for name, t, like in zip(("dq", "dk", "dv", "dg"), out, (q, q, q, g))]
     ds0 = torch.empty(st, dtype=f32, device=q.device) if want_dstate_in else None
     workspace, size = _workspace(workspace, lib.lcla_gated_backward_workspace_bytes(B, H, N, d, code), q.device)
     _run(device, lib.lcla_gated_backward, dp, *ptrs, *dims, s0, ds1, *to, _ptr(ds0), code, _ptr(workspace), size,

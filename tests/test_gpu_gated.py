@@ -38,6 +38,8 @@ def make(seed, B, N, H, d, dtype, state=True, gates="mixed"):
         g = torch.where(torch.rand(B, N, H, generator=gen, device="cuda") < 0.05, -math.inf, -0.02)
     elif gates == "all resets":
         g = torch.full((B, N, H), -math.inf, device="cuda")
+    elif gates == "growth":      # a state that grows
+        g = torch.full((B, N, H), 0.01, device="cuda")
     s0 = r(B, H, d, d) * 2 if state else None
     return q, k, v, g.contiguous(), s0
 
@@ -92,7 +94,7 @@ SHAPES = [  # B, N, H, d, state
 ]
 
 
-@pytest.mark.parametrize("gates", ["mixed", "none", "strong", "resets"])
+@pytest.mark.parametrize("gates", ["mixed", "none", "strong", "resets", "all resets", "growth"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,N,H,d,state", SHAPES)
 def test_forward(B, N, H, d, state, dtype, gates):
@@ -105,7 +107,7 @@ def test_forward(B, N, H, d, state, dtype, gates):
     within(s1, rs, As, torch.float32, 17, "state")
 
 
-@pytest.mark.parametrize("gates", ["mixed", "none", "strong", "resets"])
+@pytest.mark.parametrize("gates", ["mixed", "none", "strong", "resets", "growth"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,N,H,d,state", SHAPES)
 def test_gradient(B, N, H, d, state, dtype, gates):
@@ -127,6 +129,14 @@ def test_gradient(B, N, H, d, state, dtype, gates):
         Ag = Ag + (last * ds.double().abs()).sum((-1, -2))[:, None]
     within(got[3], ref[3], Ag, torch.float32, 17, "dg")
     assert (got[3][torch.isinf(g)] == 0).all(), "a reset has no gradient"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,d", [(9001, 32), (5003, 64)])
+def test_more_segments_than_a_scan_takes_at_once(N, d, dtype):
+    """One head of a long sequence is cut into more than 64 segments."""
+    test_forward(1, N, 1, d, True, dtype, "mixed")
+    test_gradient(1, N, 1, d, True, dtype, "none")
 
 
 def test_gradient_against_differences():
