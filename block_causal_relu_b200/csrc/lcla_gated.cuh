@@ -394,27 +394,27 @@ __device__ __forceinline__ void group_sync(int group)
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * NS) : "memory");
 }
 
-// The NS warps of a head copy 32 token rows of it into a tile; rows past N are filled with zeros.
+// The warps of a head copy 32 token rows of it into a tile; rows past N are filled with zeros.  `p` is the thread's own
+// first 16 bytes of the tile, `live` the rows before N.
 template <typename T, int D>
-__device__ __forceinline__ void copy_tile(uint32_t tile, const char *base, size_t row_bytes, int t0, int N, int tid)
+__device__ __forceinline__ void copy_tile(uint32_t tile, const char *p, size_t row_bytes, int live, int tid)
 {
     using L = Tile<T, D>;
     constexpr int NT = D;                                  // threads of a head: 32 per 32 entries
     constexpr int RPI = NT / L::PIECES;                    // rows per step
     const int piece = tid % L::PIECES, r0 = tid / L::PIECES;
-    const char *p = base + (size_t)(t0 + r0) * row_bytes + piece * 16;
-    if (t0 + TILE <= N) {
+    if (live >= TILE) {
 #pragma unroll
         for (int r = 0; r < TILE; r += RPI, p += RPI * row_bytes)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tile + L::at(r0 + r, piece)), "l"(p) : "memory");
         return;
     }
+    const char *const first = p - (size_t)r0 * row_bytes;   // the tile's first row is before N
 #pragma unroll
     for (int r = 0; r < TILE; r += RPI, p += RPI * row_bytes) {
-        const bool live = t0 + r0 + r < N;
-        const uint32_t dst = tile + L::at(r0 + r, piece);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(live ? p : base),
-                     "r"(live ? 16 : 0)
+        const bool on = r0 + r < live;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + L::at(r0 + r, piece)),
+                     "l"(on ? p : first), "r"(on ? 16 : 0)
                      : "memory");
     }
 }
@@ -576,20 +576,26 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
     const bool rev = DIR == EITHER ? r.rev : DIR == REVERSED;
     const size_t row = (size_t)w.H * D, row_bytes = row * sizeof(T);
     const size_t at = (size_t)b * w.N * row + (size_t)h * D;
-    const char *src[4] = {(const char *)((const T *)r.q + at), (const char *)((const T *)r.k + at),
-                          (const char *)((const T *)r.v + at), DOT ? (const char *)((const T *)r.x + at) : nullptr};
     const float *gp = w.g + (size_t)b * w.N * w.H + h;
-    T *out = (T *)r.out + at + 32 * slab;
     const int tid = slab * 32 + lane;
     auto tile_at = [&](int i) { return (rev ? first + n - 1 - i : first + i) * TILE; };
+    // the thread's 16 bytes of the next tile to copy, and the way to the one after it
+    const size_t own = (at + (size_t)(tile_at(0) + tid / L::PIECES) * row) * sizeof(T) + tid % L::PIECES * 16;
+    const char *src[4] = {(const char *)r.q + own, (const char *)r.k + own, (const char *)r.v + own,
+                          DOT ? (const char *)r.x + own : nullptr};
+    const long long step = (rev ? -TILE : TILE) * (long long)row_bytes;
     auto load = [&](int i) {
         if (i < n) {
             const uint32_t s = ring + (i % STAGES) * STAGE;
 #pragma unroll
-            for (int j = 0; j < TENSORS; ++j) copy_tile<T, D>(s + j * L::BYTES, src[j], row_bytes, tile_at(i), w.N, tid);
+            for (int j = 0; j < TENSORS; ++j) {
+                copy_tile<T, D>(s + j * L::BYTES, src[j], row_bytes, w.N - tile_at(i), tid);
+                src[j] += step;
+            }
         }
         commit();
     };
+    T *out = (T *)r.out + at + 32 * slab;
     auto load_g = [&](int i) {
         const int t = i < n ? tile_at(i) + lane : w.N;
         return t < w.N ? gp[(size_t)t * w.H] : 0.f;
@@ -755,15 +761,19 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
     const int first = seg * w.seg_tiles, n = min(w.seg_tiles, tiles - first);
     const size_t row = (size_t)w.H * D, row_bytes = row * sizeof(T);
     const size_t at = (size_t)b * w.N * row + (size_t)h * D;
-    const char *kp = (const char *)((const T *)key + at), *vp = (const char *)((const T *)val + at);
     const float *gp = w.g + (size_t)b * w.N * w.H + h;
     const int tid = slab * 32 + lane;
     auto tile_at = [&](int i) { return (rev ? first + n - 1 - i : first + i) * TILE; };
+    const size_t own = (at + (size_t)(tile_at(0) + tid / L::PIECES) * row) * sizeof(T) + tid % L::PIECES * 16;
+    const char *kp = (const char *)key + own, *vp = (const char *)val + own;
+    const long long step = (rev ? -TILE : TILE) * (long long)row_bytes;
     auto load = [&](int i) {
         if (i < n) {
             const uint32_t s = ring + (i % STAGES) * STAGE;
-            copy_tile<T, D>(s, kp, row_bytes, tile_at(i), w.N, tid);
-            copy_tile<T, D>(s + L::BYTES, vp, row_bytes, tile_at(i), w.N, tid);
+            copy_tile<T, D>(s, kp, row_bytes, w.N - tile_at(i), tid);
+            copy_tile<T, D>(s + L::BYTES, vp, row_bytes, w.N - tile_at(i), tid);
+            kp += step;
+            vp += step;
         }
         commit();
     };
