@@ -83,7 +83,7 @@ struct Shape {
 };
 
 // Bound by matrix instructions and issue slots together (100 mma.sync, about 7 cycles each beside other work, and some
-// 700 other instructions per tile and head at d = 32): 480p (70 heads, 32760 tokens, 587 MB) 131 us.
+// 700 other instructions per tile and head at d = 32): 480p (70 heads, 32760 tokens, 587 MB) 128 us.
 // NU: terms of a state update.  Where the state after the call comes out of the scan, the state in here only meets
 // bf16 outputs and two terms keep it exact enough for them; where it is itself an output, three do.
 template <typename T, int D, int NU>
