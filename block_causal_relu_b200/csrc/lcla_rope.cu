@@ -558,7 +558,7 @@ int set_units(NormArgs &a, int G)
 
 int check_norm(int B, int N, int H, int Hk, int d, int rd, int half, int P, const void *positions, float eps, int dtype)
 {
-    if (B < 1 || N < 0 || H < 1 || Hk < 0 || P < 1 || d < 1 || rd < 0 || rd > d || (rd & 1)) return LCLA_ERR_INVALID_ARG;
+    if (B < 1 || N < 0 || H < 1 || Hk < 0 || P < (N > 0) || d < 1 || rd < 0 || rd > d || (rd & 1)) return LCLA_ERR_INVALID_ARG;
     if (dtype != LCLA_BF16 && dtype != LCLA_F32) return LCLA_ERR_INVALID_ARG;
     if (half != 0 && half != 1) return LCLA_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || !isfinite(eps)) return LCLA_ERR_INVALID_ARG;

@@ -241,6 +241,17 @@ def test_rows_of_zeros_and_extremes():
     assert abs(float(o[0, 1].square().mean()) - 1.0) < 1e-5
 
 
+def test_no_tokens():
+    q = torch.empty(2, 0, 3, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    c, s = lcla.rotary_tables(0, 64)
+    assert c.shape == (0, 32)
+    qo, ko = lcla.qk_norm_rope(q, q, c, s, q_weight=w, k_weight=w)
+    assert qo.shape == q.shape and ko.shape == q.shape
+    *_, dw, dk = lcla.qk_norm_rope_backward(q, q, q, q, c, s, q_weight=w, k_weight=w)
+    assert float(dw.abs().max()) == 0.0 and float(dk.abs().max()) == 0.0      # sums of nothing
+
+
 def test_rows_around_the_output_are_left_alone():
     T, H, d = 37, 3, 64
     buf = torch.full((T + 2, 5 * d), 7.0, device="cuda", dtype=torch.bfloat16)

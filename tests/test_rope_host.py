@@ -77,6 +77,7 @@ def test_norm(kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(qo=A, ldqo=512), INVALID),               # in place needs the same rows
     (dict(N=0, q=None, k=None, qo=None, ko=None, rows=1), OK),
+    (dict(N=0, q=None, k=None, qo=None, ko=None, rows=0), OK), (dict(N=0, rows=-1), INVALID),
 ])
 def test_norm_only(kw, code):
     assert norm(**kw) == code
