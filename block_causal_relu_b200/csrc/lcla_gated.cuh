@@ -440,8 +440,8 @@ __device__ __forceinline__ void load_values(Values<T> &v, uint32_t vt, bool flip
 
 // S <- decay S + sum over the tile's tokens of (weight v) k^T, for the warp's 32 values and all keys.  Each tile's
 // sum starts from zero and meets the state in one rounded multiply-add: the matrix units cut off low bits as they
-// accumulate, which a long sum in them would collect.
-template <typename T, int D, int NT>
+// accumulate, which a long sum in them would collect.  LATER: the tiles come from the other end, S <- S + decay sum.
+template <typename T, int D, int NT, bool LATER = false>
 __device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, const Values<T> &v, bool flip,
                                        const Weights *w, float decay, int lane)
 {
@@ -481,7 +481,8 @@ __device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, con
                 float(&st)[4] = S[m][2 * e + n];
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
-                    const float2 r = fma2(make_float2(st[i], st[i + 1]), both(decay), make_float2(c[m][n][i], c[m][n][i + 1]));
+                    const float2 old = make_float2(st[i], st[i + 1]), sum = make_float2(c[m][n][i], c[m][n][i + 1]);
+                    const float2 r = LATER ? fma2(sum, both(decay), old) : fma2(old, both(decay), sum);
                     st[i] = r.x;
                     st[i + 1] = r.y;
                 }
@@ -750,7 +751,8 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
     if (r.state_end) write_state<D>(S, r.state_end + ((size_t)b * w.H + h) * D * D, slab, lane);
 }
 
-// What a segment adds to the state, from zero, and its decay.
+// What a segment adds to the state, from zero, and its decay.  The tiles are taken against the recurrence's direction,
+// each with the decay of those after it: the last ones read here are the first that the recurrence reads, and still in L2.
 template <typename T, int D, int NT, int STAGES>
 __device__ __forceinline__ void total(const Work &w, const void *key, const void *val, float *part, float *decays, bool rev,
                                       int b, int h, int seg, int group, int slab, int lane, uint32_t ring, Weights *wt)
@@ -763,10 +765,10 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
     const size_t at = (size_t)b * w.N * row + (size_t)h * D;
     const float *gp = w.g + (size_t)b * w.N * w.H + h;
     const int tid = slab * 32 + lane;
-    auto tile_at = [&](int i) { return (rev ? first + n - 1 - i : first + i) * TILE; };
+    auto tile_at = [&](int i) { return (rev ? first + i : first + n - 1 - i) * TILE; };
     const size_t own = (at + (size_t)(tile_at(0) + tid / L::PIECES) * row) * sizeof(T) + tid % L::PIECES * 16;
     const char *kp = (const char *)key + own, *vp = (const char *)val + own;
-    const long long step = (rev ? -TILE : TILE) * (long long)row_bytes;
+    const long long step = (rev ? TILE : -TILE) * (long long)row_bytes;
     auto load = [&](int i) {
         if (i < n) {
             const uint32_t s = ring + (i % STAGES) * STAGE;
@@ -786,6 +788,7 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
     float g = load_g(0);
     float S[2][D / 8][4] = {};
     double sum = 0.0;
+    float after = 1.f;
     for (int i = 0; i < n; ++i) {
         const float gnext = load_g(i + 1);
         double t;
@@ -798,7 +801,8 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
         const uint32_t kt = ring + (i % STAGES) * STAGE;
         Values<T> v;
         load_values<T, D>(v, kt + L::BYTES, false, slab, lane);
-        update<T, D, NT>(S, kt, v, false, wt, decay, lane);
+        update<T, D, NT, true>(S, kt, v, false, wt, after, lane);
+        after *= decay;
     }
     wait_copies<0>();
     const size_t at_s = ((size_t)seg * w.B + b) * w.H + h;
