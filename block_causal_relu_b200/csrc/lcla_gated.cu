@@ -84,9 +84,7 @@ struct Shape {
 
 // Bound by matrix instructions and issue slots together (100 mma.sync, about 7 cycles each beside other work, and some
 // 700 other instructions per tile and head at d = 32): 480p (70 heads, 32760 tokens, 587 MB) 128 us.
-// NU: terms of a state update.  Where the state after the call comes out of the scan, the state in here only meets
-// bf16 outputs and two terms keep it exact enough for them; where it is itself an output, three do.
-template <typename T, int D, int NU>
+template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
 gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
 {
@@ -94,13 +92,12 @@ gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
     using S = Smem<T, D, 3, ST>;
     const Place p = place<D>(w.H, 1);
     if (!p.live) return;
-    recur<T, D, FORWARD, false, 2, 2, NU, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                                   weights_of<S>());
+    recur<T, D, FORWARD, false, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p), weights_of<S>());
 }
 
 // dq and dk side by side: the same instructions for both directions, since two unrolled bodies together overflow the
 // instruction cache (measured at d = 64: warps waited for instructions 2.3 of 6 cycles with three bodies in a launch).
-// Their outputs also give dg, which is fp32: every factor keeps three terms.  Bound as the forward: 2 x 4680 tokens, 35
+// Bound as the forward: 2 x 4680 tokens, 35
 // heads, d = 64, bf16 169 us, dv 63 us.
 struct Roles {
     Role r[2];
@@ -114,8 +111,8 @@ gated_backward_qk_k(const __grid_constant__ Work w, const __grid_constant__ Role
     using S = Smem<T, D, 4, ST>;
     const Place p = place<D>(w.H, 2);
     if (!p.live) return;
-    recur<T, D, EITHER, true, 3, 3, 3, ST>(w, rs.r[p.role], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                           weights_of<S>());
+    recur<T, D, EITHER, true, ST>(w, rs.r[p.role], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
+                                  weights_of<S>());
 }
 
 template <typename T, int D>
@@ -126,8 +123,7 @@ gated_backward_v_k(const __grid_constant__ Work w, const __grid_constant__ Role 
     using S = Smem<T, D, 3, ST>;
     const Place p = place<D>(w.H, 1);
     if (!p.live) return;
-    recur<T, D, REVERSED, false, 2, 2, 2, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                              weights_of<S>());
+    recur<T, D, REVERSED, false, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p), weights_of<S>());
 }
 
 // What each segment adds to the state (forward: k, v; gradient: also q, do reversed).  Bound as the forward, by 48
@@ -145,7 +141,7 @@ gated_totals_k(const __grid_constant__ Work w, const __grid_constant__ Totals t,
     using S = Smem<T, D, 2, ST>;
     const Place p = place<D>(w.H, roles);
     if (!p.live) return;
-    total<T, D, 3, ST>(w, t.key[p.role], t.val[p.role], t.part[p.role], p.role ? nullptr : t.decays, p.role == 1, p.b,
+    total<T, D, ST>(w, t.key[p.role], t.val[p.role], t.part[p.role], p.role ? nullptr : t.decays, p.role == 1, p.b,
                        p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p), weights_of<S>());
 }
 
@@ -521,8 +517,7 @@ int run_forward(const void *q, const void *k, const void *v, const Work &w, cons
         r.state_end = nullptr;
     }
     using S = Smem<T, D, 3, Shape<T, D>::STAGES>;
-    constexpr int FEW = sizeof(T) == 2 ? 2 : 3;   // fp32 has one form
-    auto kernel = w.nseg > 1 ? gated_forward_k<T, D, FEW> : gated_forward_k<T, D, 3>;
+    auto kernel = gated_forward_k<T, D>;
     set_smem(kernel, S::BYTES);
     const dim3 grid(blocks<D>(w, 1), w.B);
     if (w.nseg > 1) launch_after(kernel, grid, THREADS, S::BYTES, st, w, r);

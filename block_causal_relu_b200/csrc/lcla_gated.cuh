@@ -44,8 +44,11 @@ constexpr float RESET = -1000.f;   // a log decay below this counts as this: e^-
 
 // ---------------------------------------------------------------- operands
 // A pair is two neighbouring entries of the contraction index in one lane.  In<T> holds them as given: one bf16x2
-// register, or the two tf32 terms of each float.  Co<T, NT> holds computed fp32 values: NT bf16 terms (8 bits each, so
-// 3 terms keep all 24 bits of an fp32 value and 2 keep 16), or two tf32 terms (22 bits).
+// register, or the two tf32 terms of each float.  Co<T> holds computed fp32 values (states, weighted scores and weighted
+// values): three bf16 terms of 8 bits each, which keep all 24 bits, or two tf32 terms (22 bits).  With two bf16 terms
+// some bf16 outputs were a step beside the fp32 result's rounding (480p forward: 1.1e-4 from plain fp32 in the 2-norm and
+// 211 us; with three 3.9e-5, which other orders of the sums leave, and 243 us).
+constexpr int TERMS = 3;
 template <typename T>
 struct In;
 template <>
@@ -56,12 +59,12 @@ template <>
 struct In<float> {
     uint32_t h[2], l[2];
 };
-template <typename T, int NT>
+template <typename T>
 struct Co {
-    uint32_t u[NT];
+    uint32_t u[TERMS];
 };
-template <int NT>
-struct Co<float, NT> {
+template <>
+struct Co<float> {
     uint32_t h[2], l[2];
 };
 
@@ -83,13 +86,12 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-template <int NT>
-__device__ __forceinline__ void split(Co<__nv_bfloat16, NT> &o, float2 v)
+__device__ __forceinline__ void split(Co<__nv_bfloat16> &o, float2 v)
 {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < TERMS; ++i) {
         o.u[i] = pack_bf16(v.x, v.y);
-        if (i + 1 < NT) v = fma2(make_float2(lo_f(o.u[i]), hi_f(o.u[i])), both(-1.f), v);
+        if (i + 1 < TERMS) v = fma2(make_float2(lo_f(o.u[i]), hi_f(o.u[i])), both(-1.f), v);
     }
 }
 template <typename P>
@@ -102,11 +104,7 @@ __device__ __forceinline__ void split_tf32(P &o, float2 v)
     o.l[0] = __float_as_uint(l.x);
     o.l[1] = __float_as_uint(l.y);
 }
-template <int NT>
-__device__ __forceinline__ void split(Co<float, NT> &o, float2 v)
-{
-    split_tf32(o, v);
-}
+__device__ __forceinline__ void split(Co<float> &o, float2 v) { split_tf32(o, v); }
 __device__ __forceinline__ float2 value(const In<__nv_bfloat16> &p) { return make_float2(lo_f(p.u), hi_f(p.u)); }
 __device__ __forceinline__ float2 value(const In<float> &p)
 {
@@ -148,9 +146,9 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
 // first.  A's pairs: (row l/4, k 0-7), (row l/4 + 8, k 0-7), (row l/4, k 8-15), (row l/4 + 8, k 8-15); B's: (k 0-7),
 // (k 8-15) of column l/4.  Callers take one step of several products in turn, so that no instruction waits for the one
 // before it.
-template <typename T, int NT>
+template <typename T, bool COMPUTED>   // whether one of the factors is a Co
 struct Steps {
-    static constexpr int N = sizeof(T) == 2 ? NT : 6;
+    static constexpr int N = sizeof(T) == 2 ? (COMPUTED ? TERMS : 1) : 6;
 };
 template <bool ZERO>
 __device__ __forceinline__ void mma(int, float (&c)[4], const In<__nv_bfloat16> (&a)[4], const In<__nv_bfloat16> &b0,
@@ -158,18 +156,18 @@ __device__ __forceinline__ void mma(int, float (&c)[4], const In<__nv_bfloat16> 
 {
     mma_bf16<ZERO>(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u, b1.u);
 }
-template <bool ZERO, int NT>
-__device__ __forceinline__ void mma(int step, float (&c)[4], const Co<__nv_bfloat16, NT> (&a)[4],
+template <bool ZERO>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const Co<__nv_bfloat16> (&a)[4],
                                     const In<__nv_bfloat16> &b0, const In<__nv_bfloat16> &b1)
 {
-    const int i = NT - 1 - step;
+    const int i = TERMS - 1 - step;
     mma_bf16<ZERO>(c, a[0].u[i], a[1].u[i], a[2].u[i], a[3].u[i], b0.u, b1.u);
 }
-template <bool ZERO, int NT>
+template <bool ZERO>
 __device__ __forceinline__ void mma(int step, float (&c)[4], const In<__nv_bfloat16> (&a)[4],
-                                    const Co<__nv_bfloat16, NT> &b0, const Co<__nv_bfloat16, NT> &b1)
+                                    const Co<__nv_bfloat16> &b0, const Co<__nv_bfloat16> &b1)
 {
-    const int i = NT - 1 - step;
+    const int i = TERMS - 1 - step;
     mma_bf16<ZERO>(c, a[0].u, a[1].u, a[2].u, a[3].u, b0.u[i], b1.u[i]);
 }
 // A tf32 instruction contracts 8 entries: its slots 0-3 take the first of each pair, slots 4-7 the second.
@@ -191,15 +189,15 @@ __device__ __forceinline__ void mma(int step, float (&c)[4], const In<float> (&a
 {
     mma_split<ZERO>(step, c, a, b0, b1);
 }
-template <bool ZERO, int NT>
-__device__ __forceinline__ void mma(int step, float (&c)[4], const Co<float, NT> (&a)[4], const In<float> &b0,
+template <bool ZERO>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const Co<float> (&a)[4], const In<float> &b0,
                                     const In<float> &b1)
 {
     mma_split<ZERO>(step, c, a, b0, b1);
 }
-template <bool ZERO, int NT>
-__device__ __forceinline__ void mma(int step, float (&c)[4], const In<float> (&a)[4], const Co<float, NT> &b0,
-                                    const Co<float, NT> &b1)
+template <bool ZERO>
+__device__ __forceinline__ void mma(int step, float (&c)[4], const In<float> (&a)[4], const Co<float> &b0,
+                                    const Co<float> &b1)
 {
     mma_split<ZERO>(step, c, a, b0, b1);
 }
@@ -441,11 +439,11 @@ __device__ __forceinline__ void load_values(Values<T> &v, uint32_t vt, bool flip
 // S <- decay S + sum over the tile's tokens of (weight v) k^T, for the warp's 32 values and all keys.  Each tile's
 // sum starts from zero and meets the state in one rounded multiply-add: the matrix units cut off low bits as they
 // accumulate, which a long sum in them would collect.  LATER: the tiles come from the other end, S <- S + decay sum.
-template <typename T, int D, int NT, bool LATER = false>
+template <typename T, int D, bool LATER = false>
 __device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, const Values<T> &v, bool flip,
                                        const Weights *w, float decay, int lane)
 {
-    Co<T, NT> a[2][2][4];                                // [value block][token block]
+    Co<T> a[2][2][4];                                // [value block][token block]
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
@@ -466,7 +464,7 @@ __device__ __forceinline__ void update(float (&S)[2][D / 8][4], uint32_t kt, con
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-            for (int i = 0; i < Steps<T, NT>::N; ++i)
+            for (int i = 0; i < Steps<T, true>::N; ++i)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -563,9 +561,8 @@ __device__ __forceinline__ void write_rows<__nv_bfloat16>(__nv_bfloat16 *out, si
 
 enum Direction { FORWARD, REVERSED, EITHER };   // EITHER: the role says which, so that both run the same instructions
 
-// One recurrence over one segment of one head.  NP, NQ, NU: bf16 terms of the weighted scores, of the state where it
-// meets the query, and of the weighted values of an update.
-template <typename T, int D, Direction DIR, bool DOT, int NP, int NQ, int NU, int STAGES>
+// One recurrence over one segment of one head.
+template <typename T, int D, Direction DIR, bool DOT, int STAGES>
 __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h, int seg, int group, int slab, int lane,
                                       uint32_t ring, Weights *wt)
 {
@@ -633,7 +630,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
         for (int ks = 0; ks < D / 16; ++ks) {
             load_a<D>(q[0][ks], qt, block(0), ks, lane);
             load_a<D>(q[1][ks], qt, block(1), ks, lane);
-            Co<T, NQ> s[4][2];
+            Co<T> s[4][2];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -642,7 +639,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                     split(s[c][e], make_float2(x[2 * (c & 1)], x[2 * (c & 1) + 1]));
                 }
 #pragma unroll
-            for (int j = 0; j < Steps<T, NQ>::N; ++j)
+            for (int j = 0; j < Steps<T, true>::N; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -680,14 +677,14 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                     In<T> k[2][2];
                     load_b<D>(k, kt, sb, ks, lane);
 #pragma unroll
-                    for (int i = 0; i < Steps<T, 1>::N; ++i)
+                    for (int i = 0; i < Steps<T, false>::N; ++i)
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt) {
                             if (ks == 0 && i == 0) mma<true>(i, sc[nt], q[m][ks], k[nt][0], k[nt][1]);
                             else mma<false>(i, sc[nt], q[m][ks], k[nt][0], k[nt][1]);
                         }
                 }
-                Co<T, NP> p[4];
+                Co<T> p[4];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     const int s = 16 * sb + 8 * nt + 2 * (lane & 3);
@@ -706,7 +703,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < Steps<T, NP>::N; ++i)
+                for (int i = 0; i < Steps<T, true>::N; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) mma<false>(i, acc[m][c], p, v[j][c >> 1][c & 1][0], v[j][c >> 1][c & 1][1]);
             }
@@ -745,7 +742,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
             }
             write_rows<T>(out + (size_t)t * row, row, acc[m], t, w.N, lane);
         }
-        if (i + 1 < n || r.state_end) update<T, D, NU>(S, kt, v, rev, wt, decay, lane);
+        if (i + 1 < n || r.state_end) update<T, D>(S, kt, v, rev, wt, decay, lane);
     }
     wait_copies<0>();
     if (r.state_end) write_state<D>(S, r.state_end + ((size_t)b * w.H + h) * D * D, slab, lane);
@@ -753,7 +750,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
 
 // What a segment adds to the state, from zero, and its decay.  The tiles are taken against the recurrence's direction,
 // each with the decay of those after it: the last ones read here are the first that the recurrence reads, and still in L2.
-template <typename T, int D, int NT, int STAGES>
+template <typename T, int D, int STAGES>
 __device__ __forceinline__ void total(const Work &w, const void *key, const void *val, float *part, float *decays, bool rev,
                                       int b, int h, int seg, int group, int slab, int lane, uint32_t ring, Weights *wt)
 {
@@ -801,7 +798,7 @@ __device__ __forceinline__ void total(const Work &w, const void *key, const void
         const uint32_t kt = ring + (i % STAGES) * STAGE;
         Values<T> v;
         load_values<T, D>(v, kt + L::BYTES, false, slab, lane);
-        update<T, D, NT, true>(S, kt, v, false, wt, after, lane);
+        update<T, D, true>(S, kt, v, false, wt, after, lane);
         after *= decay;
     }
     wait_copies<0>();
