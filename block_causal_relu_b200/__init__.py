@@ -175,6 +175,39 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _cuda_device(*candidates):
+    """The device of the first CUDA tensor, or None: the call itself refuses what it gets then."""
+    for t in candidates:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            return t.device
+    return None
+
+
+def _on_stream(fn, stream, device, /, *args, **kw):
+    """``fn`` with ``stream`` as the current stream, so that what it allocates is
+    that stream's memory: a block that the caller's stream has freed, with work on
+    it still queued there, is not written by another one.  The results are kept
+    from reuse until both streams are done with them."""
+    if device is None:
+        return fn(*args, **kw)
+    index = torch.device(device).index
+    index = torch.cuda.current_device() if index is None else index
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), index) if int(stream) else torch.cuda.default_stream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream must be a stream of cuda:{index}")
+    here = torch.cuda.current_stream(index)
+    if stream.cuda_stream == here.cuda_stream:
+        return fn(*args, **kw)
+    with torch.cuda.stream(stream):
+        result = fn(*args, **kw)
+    for t in (*(result if isinstance(result, tuple) else (result,)), kw.get("workspace")):
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(here)
+    return result
+
+
 def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch.Tensor,
             rope_sin: torch.Tensor, block_len: int, eps: float = DEFAULT_EPS, *,
             out: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
@@ -188,6 +221,9 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch.T
     ``events``: optional 4 already-recorded ``torch.cuda.Event(enable_timing=True)``
     that the library re-records around its passes (``lcla_forward_timed``).
     """
+    if stream is not None:
+        return _on_stream(forward, stream, _cuda_device(q), q, k, v, rope_cos, rope_sin, block_len, eps, out=out,
+                          state_out=state_out, want_state=want_state, workspace=workspace, events=events)
     B, N, H, d, code = _inputs(q, k, v, rope_cos, rope_sin)
     if out is None:
         out = torch.empty_like(q)
@@ -205,7 +241,7 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch.T
                                   B, H, N, d, int(block_len), float(eps), _ptr(out),
                                   _ptr(state_out), code, _ptr(workspace),
                                   0 if workspace is None else workspace.numel(),
-                                  _stream(stream, q.device), evp))
+                                  _stream(None, q.device), evp))
     return out, state_out
 
 
@@ -216,6 +252,9 @@ def forward_blocks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: 
                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """``lcla_forward_blocks``: as ``forward`` with explicit block boundaries,
     ``block_offsets`` an int32 CUDA tensor [nblocks + 1] rising from 0 to N."""
+    if stream is not None:
+        return _on_stream(forward_blocks, stream, _cuda_device(q), q, k, v, rope_cos, rope_sin, block_offsets, eps,
+                          out=out, state_out=state_out, want_state=want_state, workspace=workspace)
     B, N, H, d, code = _inputs(q, k, v, rope_cos, rope_sin)
     if (not isinstance(block_offsets, torch.Tensor) or not block_offsets.is_cuda
             or block_offsets.dtype != torch.int32 or block_offsets.dim() != 1
@@ -233,7 +272,7 @@ def forward_blocks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: 
                                    B, H, N, d, _ptr(block_offsets), nblocks, float(eps), _ptr(out),
                                    _ptr(state_out), code, _ptr(workspace),
                                    0 if workspace is None else workspace.numel(),
-                                   _stream(stream, q.device)))
+                                   _stream(None, q.device)))
     return out, state_out
 
 
@@ -257,6 +296,9 @@ def shard_begin(k: torch.Tensor, v: torch.Tensor, rope_cos: torch.Tensor, rope_s
     [B, N, H, d] (whole blocks of the sequence, tables at their absolute
     positions).  Returns (total [B, H, d+1, d] fp32, workspace); pass the same
     workspace to ``shard_end``."""
+    if stream is not None:
+        return _on_stream(shard_begin, stream, _cuda_device(k), k, v, rope_cos, rope_sin, block_len,
+                          total_out=total_out, workspace=workspace)
     B, N, H, d, code = _inputs(k, k, v, rope_cos, rope_sin)
     if total_out is None:
         total_out = torch.empty((B, H, d + 1, d), dtype=torch.float32, device=k.device)
@@ -266,7 +308,7 @@ def shard_begin(k: torch.Tensor, v: torch.Tensor, rope_cos: torch.Tensor, rope_s
         workspace = torch.empty(need, dtype=torch.uint8, device=k.device)
     _check(lib.lcla_shard_begin(_ptr(k), _ptr(v), _ptr(rope_cos), _ptr(rope_sin), B, H, N, d, int(block_len),
                                 _ptr(total_out), code, _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _stream(stream, k.device)))
+                                0 if workspace is None else workspace.numel(), _stream(None, k.device)))
     return total_out, workspace
 
 
@@ -280,6 +322,9 @@ def shard_end(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch
     [R, B, H, d+1, d] (every rank's ``shard_begin`` total, in rank order) and
     the workspace ``shard_begin`` filled.  Returns (out, state after the whole
     sequence, or None)."""
+    if stream is not None:
+        return _on_stream(shard_end, stream, _cuda_device(q), q, k, v, rope_cos, rope_sin, block_len, totals, rank,
+                          workspace, eps, state_in=state_in, out=out, state_out=state_out, want_state=want_state)
     B, N, H, d, code = _inputs(q, k, v, rope_cos, rope_sin)
     if not isinstance(totals, torch.Tensor) or totals.dim() != 5:
         raise ValueError("totals must be [R, B, H, d+1, d]")
@@ -294,7 +339,7 @@ def shard_end(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch
     _check(lib.lcla_shard_end(_ptr(q), _ptr(k), _ptr(v), _ptr(rope_cos), _ptr(rope_sin), B, H, N, d,
                               int(block_len), float(eps), _ptr(totals), nranks, int(rank), _ptr(state_in),
                               _ptr(out), _ptr(state_out), code, _ptr(workspace),
-                              0 if workspace is None else workspace.numel(), _stream(stream, q.device)))
+                              0 if workspace is None else workspace.numel(), _stream(None, q.device)))
     return out, state_out
 
 
@@ -321,6 +366,9 @@ def step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor,
          stream=None) -> torch.Tensor:
     """``lcla_step``: one block [B, L, H, d] against ``state`` [B, H, d+1, d]
     fp32 (updated in place when ``save``).  Returns the block's outputs."""
+    if stream is not None:
+        return _on_stream(step, stream, _cuda_device(q), q, k, v, cos, sin, state, save, eps, out=out,
+                          workspace=workspace)
     B, L, H, d, code = _inputs(q, k, v, cos, sin)
     if (not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous()
             or tuple(state.shape) != (B, H, d + 1, d)):
@@ -332,7 +380,7 @@ def step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor,
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(lib.lcla_step(_ptr(q), _ptr(k), _ptr(v), _ptr(cos), _ptr(sin), B, H, L, d, float(eps),
                          _ptr(state), int(bool(save)), _ptr(out), code, _ptr(workspace),
-                         0 if workspace is None else workspace.numel(), _stream(stream, q.device)))
+                         0 if workspace is None else workspace.numel(), _stream(None, q.device)))
     return out
 
 
@@ -343,6 +391,9 @@ def temporal_conv(x: torch.Tensor, tokens_per_frame: int, weight: torch.Tensor,
     frames of ``x`` [B, F * S, C] (S = ``tokens_per_frame``), with weight [2, C]
     and bias [C] fp32 and the previous frame from ``cache`` [B, S, C] (zeros
     when None); ``save`` overwrites the cache with x's last frame."""
+    if stream is not None:
+        return _on_stream(temporal_conv, stream, _cuda_device(x), x, tokens_per_frame, weight, bias, cache, save,
+                          out=out)
     if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous() or x.dim() != 3:
         raise ValueError("x must be a contiguous CUDA tensor [B, F * S, C]")
     B, N, C = x.shape
@@ -361,7 +412,7 @@ def temporal_conv(x: torch.Tensor, tokens_per_frame: int, weight: torch.Tensor,
     if out is None:
         out = torch.empty_like(x)
     _check(lib.lcla_temporal_conv(_ptr(x), B, N // S, S, C, _ptr(weight), _ptr(bias), _ptr(cache),
-                                  int(bool(save)), _ptr(out), code, _stream(stream, x.device)))
+                                  int(bool(save)), _ptr(out), code, _stream(None, x.device)))
     return out
 
 
@@ -391,18 +442,6 @@ def _array(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtyp
     return t.data_ptr()
 
 
-def _hold(stream, device: int, *tensors) -> None:
-    """Memory made here on the current stream for work on another one is not
-    given out again before that work has run."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-
-
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -417,6 +456,11 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     stand at ``positions`` [axes, n] ([n] for one axis) int64, or at indices
     ``first`` .. ``first + n - 1`` of a row-major grid whose inner axes have
     the sizes ``extents``.  ``scaling``: "none", "linear", "ntk" or "yarn"."""
+    if stream is not None:
+        return _on_stream(rotary_tables, stream, _cuda_device(positions, *(out or ())) or device, n, dims,
+                          extents=extents, first=first, positions=positions, theta=theta, scaling=scaling,
+                          factor=factor, original_len=original_len, beta_fast=beta_fast, beta_slow=beta_slow,
+                          device=device, out=out)
     dims = [int(x) for x in ([dims] if isinstance(dims, int) else dims)]
     extents = None if extents is None else [int(x) for x in extents]
     n = int(n)
@@ -450,8 +494,7 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     ints = ctypes.c_int * 3
     _run(index, lib.lcla_rotary_tables, pos, int(first), n, len(dims), ints(*dims),
          None if extents is None else ints(*extents), float(theta), ROPE_SCALING[scaling], float(factor),
-         float(original_len), float(beta_fast), float(beta_slow), *ptrs, _stream(stream, index))
-    _hold(stream, index, *out)
+         float(original_len), float(beta_fast), float(beta_slow), *ptrs, _stream(None, index))
     return out[0], out[1]
 
 
@@ -527,10 +570,12 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], rope_cos: torch.Ten
     2 * rope_cos.shape[1] entries by the table rows at ``positions`` [B, N]
     int64 (token n's own row without).  q and k may be column windows of one
     projection; ``out`` = (q_out, k_out) may be (q, k) themselves."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope, stream, _cuda_device(q), q, k, rope_cos, rope_sin, q_weight=q_weight,
+                          k_weight=k_weight, eps=eps, positions=positions, half_layout=half_layout, out=out)
     ins, tail, code, device = _norm_call(q, k, rope_cos, rope_sin, q_weight, k_weight, positions, eps, half_layout)
     out, to = _norm_out(q, k, out)
-    _run(device, lib.lcla_qk_norm_rope, *ins, *tail, *to, code, _stream(stream, device))
-    _hold(stream, device, *out)
+    _run(device, lib.lcla_qk_norm_rope, *ins, *tail, *to, code, _stream(None, device))
     return out
 
 
@@ -543,6 +588,10 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
     """``lcla_qk_norm_rope_backward``: (dq, dk, dq_weight, dk_weight) from the
     gradients of ``qk_norm_rope``'s outputs and its inputs; a weight that was
     not given has no gradient (None)."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope_backward, stream, _cuda_device(q), dq_out, dk_out, q, k, rope_cos, rope_sin,
+                          q_weight=q_weight, k_weight=k_weight, eps=eps, positions=positions, half_layout=half_layout,
+                          out=out, workspace=workspace)
     ins, tail, code, device = _norm_call(q, k, rope_cos, rope_sin, q_weight, k_weight, positions, eps, half_layout)
     ldgq = _rows("dq_out", dq_out, q)
     ldgk = 0 if k is None else _rows("dk_out", dk_out, k)
@@ -552,8 +601,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
     workspace, size = _workspace(workspace, 0 if dqw is None and dkw is None else
                                  lib.lcla_qk_norm_rope_backward_workspace_bytes(q.shape[3]), q.device)
     _run(device, lib.lcla_qk_norm_rope_backward, dq_out.data_ptr(), ldgq, None if k is None else dk_out.data_ptr(),
-         ldgk, *ins, *tail, *to, _ptr(dqw), _ptr(dkw), code, _ptr(workspace), size, _stream(stream, device))
-    _hold(stream, device, *out, dqw, dkw, workspace)
+         ldgk, *ins, *tail, *to, _ptr(dqw), _ptr(dkw), code, _ptr(workspace), size, _stream(None, device))
     return out[0], out[1], dqw, dkw
 
 
@@ -600,6 +648,9 @@ def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     scale S_t q_t over q, k, v [B, N, H, d] with log decays g [B, N, H] fp32 and
     scale d^-1/2 unless given.  Returns (out, state after the last token
     [B, H, d, d] fp32 or None)."""
+    if stream is not None:
+        return _on_stream(gated_forward, stream, _cuda_device(q), q, k, v, g, scale, state_in=state_in, out=out,
+                          state_out=state_out, want_state=want_state, workspace=workspace)
     ptrs, dims, code, device = _gated_inputs(q, k, v, g, scale)
     B, H, N, d, _ = dims
     st = (B, H, d, d)
@@ -616,8 +667,7 @@ def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         s1 = _array("state_out", state_out, st, torch.float32, device)
     workspace, size = _workspace(workspace, _gated_need(B, H, N, d, code), q.device)
     _run(device, lib.lcla_gated_forward, *ptrs, *dims, s0, op, s1, code, _ptr(workspace), size,
-         _stream(stream, device))
-    _hold(stream, device, out, state_out, workspace)
+         _stream(None, device))
     return out, state_out
 
 
@@ -628,11 +678,14 @@ def gated_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     """``lcla_gated_step``: one block [B, L, H, d] (one token, when serving)
     against ``state`` [B, H, d, d] fp32.  With ``save`` the state after the block
     goes to ``state_out``, or to ``state`` itself.  Returns the block's outputs."""
+    if stream is not None:
+        return _on_stream(gated_step, stream, _cuda_device(q), q, k, v, g, state, save, scale, state_out=state_out,
+                          out=out, workspace=workspace)
     if state is None:
         raise TypeError("state must be a CUDA tensor")
     if state_out is not None:
         return gated_forward(q, k, v, g, scale, state_in=state, out=out, state_out=state_out if save else None,
-                             want_state=False, workspace=workspace, stream=stream)[0]
+                             want_state=False, workspace=workspace)[0]
     ptrs, dims, code, device = _gated_inputs(q, k, v, g, scale)
     B, H, L, d, _ = dims
     sp = _array("state", state, (B, H, d, d), torch.float32, device)
@@ -643,8 +696,7 @@ def gated_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
         op = _array("out", out, q.shape, q.dtype, device)
     workspace, size = _workspace(workspace, _gated_need(B, H, L, d, code), q.device)
     _run(device, lib.lcla_gated_step, *ptrs, *dims, sp, 1 if save else 0, op, code, _ptr(workspace), size,
-         _stream(stream, device))
-    _hold(stream, device, out, workspace)
+         _stream(None, device))
     return out
 
 
@@ -656,6 +708,9 @@ def gated_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     """``lcla_gated_backward``: (dq, dk, dv, dg, dstate_in or None) from the
     gradients of ``gated_forward``'s outputs and its inputs; ``out`` gives the
     buffers of the first four."""
+    if stream is not None:
+        return _on_stream(gated_backward, stream, _cuda_device(q), dout, q, k, v, g, scale, state_in=state_in,
+                          dstate_out=dstate_out, want_dstate_in=want_dstate_in, out=out, workspace=workspace)
     ptrs, dims, code, device = _gated_inputs(q, k, v, g, scale)
     B, H, N, d, _ = dims
     if dout is None:
@@ -673,6 +728,5 @@ def gated_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     ds0 = torch.empty(st, dtype=f32, device=q.device) if want_dstate_in else None
     workspace, size = _workspace(workspace, lib.lcla_gated_backward_workspace_bytes(B, H, N, d, code), q.device)
     _run(device, lib.lcla_gated_backward, dp, *ptrs, *dims, s0, ds1, *to, _ptr(ds0), code, _ptr(workspace), size,
-         _stream(stream, device))
-    _hold(stream, device, *out, ds0, workspace)
+         _stream(None, device))
     return (*out, ds0)
