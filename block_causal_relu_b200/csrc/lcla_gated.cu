@@ -221,45 +221,196 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) gated_scan_k(const __grid_con
 }
 
 struct GradGate {
-    const float *g;
-    const float *dot;          // [planes][B, H, N]
+    const void *q, *k, *v, *dout;
+    float *dot;                // [planes][B, H, N]: as the roles left them, queries' planes first
+    const float *norm;         // [planes][B, H, tiles]
+    float *up, *down, *most;   // [B, H, tiles], strong tiles: sum of A, sum of B, the bound of X
     const float *before;       // [nseg + 1][B, H, d, d]: the state before each segment, and after the last
     const float *after;        // [nseg][B, H, d, d]: its gradient after each segment, over scale
     float *dg;
-    int B, H, N, nseg, seg_tiles;
-    float scale;
+    Work w;
+    bool carried;              // a state came in before the first token
 };
 
-// dg_t = <S, R> at the segment's end + the sum over the segment's tokens from t on of <q, dq> - <k, dk>.  The sum over
-// all later tokens would be the same number, as a difference of two long sums that nearly cancel; starting again at
-// each segment's end keeps it to 32-bit accuracy.  One block per segment of a head (at most 32 tiles): each warp takes
-// every fourth tile, latest first, reads all of them at once and sums each from its end.
+// Two neighbouring entries of one token's row in global memory, or zeros.
+__device__ __forceinline__ In<__nv_bfloat16> pair_of(const __nv_bfloat16 *p, bool on)
+{
+    return In<__nv_bfloat16>{on ? *reinterpret_cast<const uint32_t *>(p) : 0u};
+}
+__device__ __forceinline__ In<float> pair_of(const float *p, bool on)
+{
+    In<float> r;
+    split_tf32(r, on ? *reinterpret_cast<const float2 *>(p) : make_float2(0.f, 0.f));
+    return r;
+}
+
+// Products of a tile's rows a_u . b_s for the 16x16 blocks (0,0), (1,0) and (1,1), whose first rows lie at a and b.
+template <typename T, int D>
+__device__ __forceinline__ void tile_scores(float (&c)[3][2][4], const T *a, const T *b, size_t row, int live, int lane)
+{
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        In<T> fa[2][4], fb[2][2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int u = 16 * m + 8 * (p & 1) + (lane >> 2), e = 16 * ks + 8 * (p >> 1) + 2 * (lane & 3);
+                fa[m][p] = pair_of(a + u * row + e, u < live);
+                const int s = 16 * m + 8 * (p >> 1) + (lane >> 2), f = 16 * ks + 8 * (p & 1) + 2 * (lane & 3);
+                fb[m][p >> 1][p & 1] = pair_of(b + s * row + f, s < live);
+            }
+#pragma unroll
+        for (int i = 0; i < Steps<T, false>::N; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (ks == 0 && i == 0) {
+                    mma<true>(i, c[0][n], fa[0], fb[0][n][0], fb[0][n][1]);
+                    mma<true>(i, c[1][n], fa[1], fb[0][n][0], fb[0][n][1]);
+                    mma<true>(i, c[2][n], fa[1], fb[1][n][0], fb[1][n][1]);
+                } else {
+                    mma<false>(i, c[0][n], fa[0], fb[0][n][0], fb[0][n][1]);
+                    mma<false>(i, c[1][n], fa[1], fb[0][n][0], fb[0][n][1]);
+                    mma<false>(i, c[2][n], fa[1], fb[1][n][0], fb[1][n][1]);
+                }
+            }
+    }
+}
+
+// In lane t: the sum of M[u][s] over s < t <= u inside the tile, M[u][s] = e^{G_u - G_s} (q_u . k_s) (do_u . v_s).
+constexpr int kPairRow = TILE + 1;
+template <typename T, int D>
+__device__ __forceinline__ float tile_pairs(const GradGate &p, size_t at, size_t row, int live, const Weights *wt,
+                                            float *M, int lane)
+{
+    float qk[3][2][4], dv[3][2][4];
+    tile_scores<T, D>(qk, (const T *)p.q + at, (const T *)p.k + at, row, live, lane);
+    tile_scores<T, D>(dv, (const T *)p.dout + at, (const T *)p.v + at, row, live, lane);
+    __syncwarp();                              // the last tile's sums have been read
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int u = 16 * (i > 0) + 8 * (j >> 1) + (lane >> 2);
+                const int s = 16 * (i > 1) + 8 * n + 2 * (lane & 3) + (j & 1);
+                const float e = (wt->whole[s] - wt->whole[u]) + (wt->frac[s] - wt->frac[u]);
+                M[u * kPairRow + s] = qk[i][n][j] * dv[i][n][j] * ex2(e);
+            }
+    __syncwarp();
+    float x[TILE], sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < TILE; ++s) x[s] = M[lane * kPairRow + s];
+#pragma unroll
+    for (int s = 0; s < TILE; ++s) {           // row `lane`: M[u][t] becomes the sum over s < t
+        M[lane * kPairRow + s] = sum;
+        sum += s < lane ? x[s] : 0.f;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < TILE; ++u) x[u] = M[u * kPairRow + lane];
+    sum = 0.f;
+#pragma unroll
+    for (int u = TILE - 1; u >= 0; --u) sum += u >= lane ? x[u] : 0.f;
+    return sum;
+}
+
+// dg_t is scale times the sum of M[u][s] (above) over all pairs s < t <= u of the sequence, the carried state and the
+// carried gradient counting as tokens at its ends.  The value at a segment's end is <S, R>; from a token to the one before
+// it the sum changes by <q, dq> - <k, dk>.  Where a state decays much between two tokens those terms cancel to less than
+// their own roundings, and a running sum would carry the roundings of later tokens to ones that they cannot reach.  So
+// tiles go by their decay (strong_tile):
+//   mild: the running sum;
+//   strong: with D the value after the tile, A_u and B_s the carried states' parts of <q_u, dq_u> and <k_s, dk_s>, and X
+//     the pairs around the whole tile,
+//       X = D - sum of all B_s, no larger than decay |S before| |R after|,
+//       dg_t = X + sum over u >= t of A_u + sum over s < t of B_s + the pairs inside the tile,
+//     each a sum over pairs of dg_t alone, and nothing at all across a decay that is zero.
+// What errors are left, beside 2^-17 of the magnitudes of dg_t's own pairs: in a mild tile 2^-22 of the terms of the mild
+// tiles after it; in X the same of the pairs around the tile's end, never more than its bound (so a single gate of g < -3
+// among mild ones has the roundings of its neighbours, 2^-22 e^-g of itself).
+// gated_dgate_strong_k, a warp per tile, does what a strong one needs and leaves its part of dg in the first plane;
+// gated_dgate_k, a block per segment of a head (at most 32 tiles), takes D through the segment.  Bound by latency: 2 x 4680
+// tokens, 35 heads, d = 64, bf16, 6 % of the tiles strong, 15 and 13 us from cold caches; all of them strong 66 us more.
+template <typename T, int D>
+__global__ void __launch_bounds__(THREADS) gated_dgate_strong_k(const __grid_constant__ GradGate p)
+{
+    constexpr int PLANES = D / 32;
+    __shared__ Weights weights[WARPS];
+    __shared__ float pairs[WARPS][TILE * kPairRow];
+    after_launch_before();
+    const Work &w = p.w;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = w.B * w.H, tiles = (w.N + TILE - 1) / TILE;
+    const size_t nplane = (size_t)BH * tiles, unit = (size_t)blockIdx.x * WARPS + warp;
+    if (unit >= nplane || p.norm[unit] == -1.f) return;
+    const int tile = (int)(unit % tiles), bh = (int)(unit / tiles), b = bh / w.H, h = bh % w.H;
+    const int t0 = tile * TILE, t = t0 + lane, u = min(t, w.N - 1);
+    const size_t plane = (size_t)BH * w.N, row = (size_t)w.H * D;
+    float *dot = p.dot + (size_t)bh * w.N + u;
+    float g = w.g[((size_t)b * w.N + u) * w.H + h], A = 0.f, B = 0.f;
+#pragma unroll
+    for (int k = 0; k < PLANES; ++k) {
+        A += dot[k * plane];
+        B -= dot[(PLANES + k) * plane];        // <k, dk>, which its planes hold negated
+    }
+    if (t >= w.N) A = B = g = 0.f;
+    double total;
+    const float decay = tile_weights(&weights[warp], g, false, lane, total);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {         // sums from each token on, and up to each token
+        const float later = __shfl_down_sync(0xffffffffu, A, o), earlier = __shfl_up_sync(0xffffffffu, B, o);
+        if (lane + o < 32) A += later;
+        if (lane >= o) B += earlier;
+    }
+    if (lane == 0) p.up[unit] = A;
+    if (lane == 31) {
+        float sq = 0.f, rq = 0.f;
+#pragma unroll
+        for (int k = 0; k < PLANES; ++k) {
+            sq += p.norm[k * nplane + unit];
+            rq += p.norm[(PLANES + k) * nplane + unit];
+        }
+        p.down[unit] = B;
+        // 1.001: the bound's own roundings
+        p.most[unit] = decay == 0.f ? 0.f : 1.001f * decay * fabsf(w.scale) * sqrtf(sq) * sqrtf(rq);
+    }
+    const float pair = tile_pairs<T, D>(p, ((size_t)b * w.N + t0) * row + (size_t)h * D, row, min(TILE, w.N - t0),
+                                        &weights[warp], pairs[warp], lane);
+    const float before = __shfl_up_sync(0xffffffffu, B, 1);
+    // nothing passes a reset: X is zero too
+    if (t < w.N) *dot = g < RESET ? 0.f : A + (lane ? before : 0.f) + w.scale * pair;
+}
+
 constexpr int kGateTiles = 32;     // tiles of a segment at most
 template <int D>
 __global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__ GradGate p)
 {
-    constexpr int PLANES = 2 * (D / 32), N4 = D * D / 4;
+    constexpr int PLANES = 2 * (D / 32), N4 = D * D / 4, PER = kGateTiles / WARPS;
+    __shared__ float ends[WARPS], up[kGateTiles], down[kGateTiles], most[kGateTiles];   // most < 0: a mild tile
     after_launch_before();
-    constexpr int PER = kGateTiles / WARPS;
-    __shared__ float sums[kGateTiles + WARPS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = p.B * p.H;
-    const int bh = (int)(blockIdx.x % (unsigned)BH), seg = (int)(blockIdx.x / (unsigned)BH), b = bh / p.H, h = bh % p.H;
-    const int t0 = seg * p.seg_tiles * TILE, t1 = min(p.N, t0 + p.seg_tiles * TILE);
-    const size_t plane = (size_t)BH * p.N;
-    const float *dot = p.dot + (size_t)bh * p.N;
-    float d[PER], g[PER];
+    const Work &w = p.w;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = w.B * w.H, tiles = (w.N + TILE - 1) / TILE;
+    const int bh = (int)(blockIdx.x % (unsigned)BH), seg = (int)(blockIdx.x / (unsigned)BH), b = bh / w.H, h = bh % w.H;
+    const int first = seg * w.seg_tiles, n = min(w.seg_tiles, tiles - first), end = first + n - 1;
+    const size_t plane = (size_t)BH * w.N;
+    const float *dot = p.dot + (size_t)bh * w.N;
+    float own[PER], rest[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int t = t1 - 1 - lane - 32 * (warp + WARPS * i);    // lane 0 has the latest token
-        const int u = max(t, t0);                                 // loads without branches go out together
-        float v[PLANES];
+    for (int i = 0; i < PER; ++i) {            // loads without branches go out together
+        const int t = (end - (warp + WARPS * i)) * TILE + lane, u = min(max(t, 0), w.N - 1);
+        own[i] = dot[u];
+        rest[i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < PLANES; ++k) v[k] = dot[k * plane + u];
-        g[i] = p.g[((size_t)b * p.N + u) * p.H + h];
-        d[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < PLANES; ++k) d[i] += v[k];
-        if (t < t0) d[i] = 0.f;
+        for (int k = 1; k < PLANES; ++k) rest[i] += dot[k * plane + u];
+        if (t >= w.N) own[i] = rest[i] = 0.f;
+    }
+    if (warp == 0 && lane < n) {
+        const size_t at = (size_t)bh * tiles + end - lane;
+        const bool strong = p.norm[at] != -1.f;
+        up[lane] = p.up[at];                   // of a mild tile: replaced below
+        down[lane] = p.down[at];
+        most[lane] = strong ? p.most[at] : -1.f;
     }
     const float4 *S = reinterpret_cast<const float4 *>(p.before) + ((size_t)(seg + 1) * BH + bh) * N4;
     const float4 *R = reinterpret_cast<const float4 *>(p.after) + ((size_t)seg * BH + bh) * N4;
@@ -271,29 +422,37 @@ __global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (lane == 0) sums[kGateTiles + warp] = y;
+    if (lane == 0) ends[warp] = y;
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
+        const int k = warp + WARPS * i;
+        if (k < n && most[k] < 0.f) {
+            float x = own[i] + rest[i];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float up = __shfl_up_sync(0xffffffffu, d[i], o);
-            if (lane >= o) d[i] += up;
+            for (int o = 1; o < 32; o <<= 1) {
+                const float later = __shfl_down_sync(0xffffffffu, x, o);
+                if (lane + o < 32) x += later;
+            }
+            own[i] = x;
+            if (lane == 0) up[k] = x;
         }
-        if (lane == 31) sums[warp + WARPS * i] = d[i];
     }
     __syncthreads();
-    double carry = 0.0;
+    double after = 0.0;                        // the value after a tile
 #pragma unroll
-    for (int k = 0; k < WARPS; ++k) carry += sums[kGateTiles + k];
-    carry *= p.scale;
+    for (int k = 0; k < WARPS; ++k) after += ends[k];
+    after *= w.scale;
 #pragma unroll
-    for (int k = 0; k < kGateTiles; ++k) {
-        if (k % WARPS == warp) {
-            const int i = k / WARPS, t = t1 - 1 - lane - 32 * k;
-            if (t >= t0) p.dg[((size_t)b * p.N + t) * p.H + h] = g[i] < RESET ? 0.f : (float)(carry + d[i]);
+    for (int k = 0; k < kGateTiles; ++k)
+        if (k < n) {
+            const float m = most[k];
+            const double X = m < 0.f ? after : fmin(fmax(after - down[k], -(double)m), (double)m);
+            const int t = (end - k) * TILE + lane;
+            if (k % WARPS == warp && t < w.N)
+                p.dg[((size_t)b * w.N + t) * w.H + h] = t == 0 && !p.carried ? 0.f : (float)(X + own[k / WARPS]);
+            after = X + up[k];
         }
-        carry += sums[k];
-    }
 }
 
 // A few tokens against the state: read once, kept in registers, written once.  One block per head; D / 4 lanes hold a
@@ -351,7 +510,7 @@ bool is_short(int N, int dtype) { return N <= (dtype == LCLA_BF16 ? 4 : 8); }
 
 struct Plan {
     int nseg, seg_tiles;
-    size_t before, after, decays, dot, bytes;   // workspace offsets
+    size_t before, after, decays, dot, norm, sums, bytes;   // workspace offsets
 };
 
 // Microseconds of a tile step of the forward's recurrence with one block on an SM, whose warps wait for one instruction
@@ -423,6 +582,10 @@ Plan make_plan(int B, int H, int N, int d, int dtype, bool backward)
         at += round_up(p.nseg * slice);
         p.dot = at;
         at += round_up((size_t)2 * ns * B * H * N * sizeof(float));
+        p.norm = at;
+        at += round_up((size_t)2 * ns * B * H * tiles * sizeof(float));
+        p.sums = at;
+        at += round_up((size_t)3 * B * H * tiles * sizeof(float));
     }
     p.bytes = at;
     return p;
@@ -531,7 +694,7 @@ int run_backward(const void *dout, const void *q, const void *k, const void *v, 
                  float *dstate_in, unsigned char *ws, cudaStream_t st)
 {
     float *before = reinterpret_cast<float *>(ws + p.before), *after = reinterpret_cast<float *>(ws + p.after);
-    float *dot = reinterpret_cast<float *>(ws + p.dot);
+    float *dot = reinterpret_cast<float *>(ws + p.dot), *norm = reinterpret_cast<float *>(ws + p.norm);
     const int BH = w.B * w.H, ns = D / 32;
     Totals t = {};
     t.key[0] = k; t.val[0] = v; t.part[0] = before;
@@ -549,14 +712,15 @@ int run_backward(const void *dout, const void *q, const void *k, const void *v, 
     s.last_scale[1] = w.scale;
     s.nseg = w.nseg; s.BH = BH; s.n4 = D * D / 4;
     launch_scan(s, 2, st);
-    const size_t plane = (size_t)BH * w.N;
+    const size_t plane = (size_t)BH * w.N, nplane = (size_t)BH * ((w.N + TILE - 1) / TILE);
     Roles rs = {};
     // recur reads the state of segment `seg` also where there is only one
     Role &rq = rs.r[0], &rk = rs.r[1], rv = {};
     rq.q = dout; rq.k = v; rq.v = k; rq.x = q; rq.out = dq;
-    rq.state = before; rq.transposed = true; rq.dot = dot; rq.sign = 1.f;
+    rq.state = before; rq.transposed = true; rq.dot = dot; rq.norm = norm; rq.sign = 1.f;
     rk.q = v; rk.k = dout; rk.v = q; rk.x = k; rk.out = dk;
-    rk.state = after; rk.transposed = true; rk.dot = dot + ns * plane; rk.sign = -1.f;
+    rk.state = after; rk.transposed = true; rk.dot = dot + ns * plane; rk.norm = norm + ns * nplane;
+    rk.sign = -1.f;
     rk.rev = true;
     rv.q = k; rv.k = q; rv.v = dout; rv.out = dv;
     rv.state = after; rv.rev = true;
@@ -567,9 +731,14 @@ int run_backward(const void *dout, const void *q, const void *k, const void *v, 
     set_smem(gated_backward_v_k<T, D>, S3::BYTES);
     launch_after(gated_backward_v_k<T, D>, dim3(blocks<D>(w, 1), w.B), THREADS, S3::BYTES, st, w, rv);
     GradGate gg = {};
-    gg.g = w.g; gg.dot = dot; gg.before = before; gg.after = after; gg.dg = dg;
-    gg.B = w.B; gg.H = w.H; gg.N = w.N; gg.nseg = w.nseg; gg.seg_tiles = w.seg_tiles;
-    gg.scale = w.scale;
+    gg.q = q; gg.k = k; gg.v = v; gg.dout = dout;
+    gg.dot = dot; gg.norm = norm; gg.before = before; gg.after = after; gg.dg = dg;
+    gg.up = reinterpret_cast<float *>(ws + p.sums);
+    gg.down = gg.up + nplane;
+    gg.most = gg.down + nplane;
+    gg.w = w;
+    gg.carried = state_in != nullptr;
+    launch_after(gated_dgate_strong_k<T, D>, dim3((unsigned)((nplane + WARPS - 1) / WARPS)), THREADS, 0, st, gg);
     launch_after(gated_dgate_k<D>, dim3((unsigned)((long long)BH * w.nseg)), THREADS, 0, st, gg);
     return launched();
 }

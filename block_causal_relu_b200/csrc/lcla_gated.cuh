@@ -315,7 +315,10 @@ struct Role {
     const void *q, *k, *v;   // query, key, value [B, N, H, d]
     const void *x;           // dot: the tensor whose rows meet the output's, or NULL
     void *out;
-    float *dot;              // [d / 32][B, H, N]: sign * <x, out> over each 32 entries
+    float *dot;              // [d / 32][B, H, N]: sign * <x, out> over each 32 entries; in a strong tile with the carried
+                             // state's part of out alone
+    float *norm;             // [d / 32][B, H, tiles]: sum of squares of the state before a strong tile, 32 rows each, or
+                             // -1 where the tile is mild
     const float *state;      // state before each segment [nseg][B, H, d, d], or of the whole call (nseg = 1), or NULL (zero)
     float *state_end;        // nseg = 1: the state after the last token, or NULL
     float sign;
@@ -383,6 +386,13 @@ __device__ __forceinline__ float tile_weights(Weights *w, float g, bool rev, int
     w->out[lane] = rev ? fromstart : toend;
     __syncwarp();
     return exact_ex2(ea, eb);
+}
+
+// Whether a tile is strong, for the gates' gradient: it keeps less than e^-3 of a state, or one of its tokens less than
+// e^-1.  Lanes hold the log decays, lane 31 in `total` the tile's G / ln 2.
+__device__ __forceinline__ bool strong_tile(float g, double total, int lane)
+{
+    return __any_sync(0xffffffffu, g < -1.f || (lane == 31 && total < -3.0 * 1.4426950408889634));
 }
 
 template <int NS>
@@ -613,6 +623,7 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
         const float gnext = load_g(i + 1);
         double total;
         const float decay = tile_weights(wt, g, rev, lane, total);
+        const bool strong = DOT && strong_tile(g, total, lane);
         g = gnext;
         wait_copies<STAGES - 2>();
         group_sync<NS>(group);               // this tile has landed for every warp, and the last one's slot is free
@@ -648,6 +659,56 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
                         else mma<false>(j, acc[m][c], q[m][ks], s[c][0], s[c][1]);
                     }
         }
+        // <x, out> over the warp's entries of a row: block m, rows l/4 + 8 hh
+        auto dot = [&](int m, int hh) {
+            float s = 0.f;
+            const int rr = 16 * block(m) + 8 * hh + (lane >> 2);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int col = 32 * slab + 8 * c + 2 * (lane & 3);
+                float2 x;
+                if (sizeof(T) == 4) {
+                    x = lds2(xt + L::at(rr, col >> 2) + 4 * (col & 3));
+                } else {
+                    const uint32_t u = lds_u(xt + L::at(rr, col >> 3) + 2 * (col & 7));
+                    x = make_float2(lo_f(u), hi_f(u));
+                }
+                s = fmaf(x.x, acc[m][c][2 * hh], s);
+                s = fmaf(x.y, acc[m][c][2 * hh + 1], s);
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            return s + __shfl_xor_sync(0xffffffffu, s, 2);
+        };
+        auto put_dot = [&](int m, int hh, float s) {
+            const int t = t0 + 16 * block(m) + 8 * hh + (lane >> 2);
+            if ((lane & 3) == 0 && t < w.N) r.dot[(((size_t)slab * w.B + b) * w.H + h) * w.N + t] = r.sign * s;
+        };
+        // A strong tile: the dots of the carried state's part, and that state's norm.  In one place, so that the products
+        // below are not split by branches.
+        float norm = -1.f;
+        if (strong) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const float in = wt->in[16 * block(m) + 8 * hh + (lane >> 2)] * w.scale;
+                    put_dot(m, hh, dot(m, hh) * in);
+                }
+            float2 sq = both(0.f);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        const float2 x = make_float2(S[m][c][j], S[m][c][j + 1]);
+                        sq = fma2(x, x, sq);
+                    }
+            norm = sq.x + sq.y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o);
+        }
+        if (DOT && lane == 0) r.norm[(((size_t)slab * w.B + b) * w.H + h) * tiles + t0 / TILE] = norm;
         // the tile's own part
         Values<T> v;
         load_values<T, D>(v, vt, rev, slab, lane);
@@ -707,7 +768,6 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
 #pragma unroll
                     for (int c = 0; c < 4; ++c) mma<false>(i, acc[m][c], p, v[j][c >> 1][c & 1][0], v[j][c >> 1][c & 1][1]);
             }
-            const int t = t0 + row0 + (lane >> 2);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -719,27 +779,11 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
             if (DOT) {
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    float s = 0.f;
-                    const int rr = row0 + 8 * hh + (lane >> 2);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int col = 32 * slab + 8 * c + 2 * (lane & 3);
-                        float2 x;
-                        if (sizeof(T) == 4) {
-                            x = lds2(xt + L::at(rr, col >> 2) + 4 * (col & 3));
-                        } else {
-                            const uint32_t u = lds_u(xt + L::at(rr, col >> 3) + 2 * (col & 7));
-                            x = make_float2(lo_f(u), hi_f(u));
-                        }
-                        s = fmaf(x.x, acc[m][c][2 * hh], s);
-                        s = fmaf(x.y, acc[m][c][2 * hh + 1], s);
-                    }
-                    s += __shfl_xor_sync(0xffffffffu, s, 1);
-                    s += __shfl_xor_sync(0xffffffffu, s, 2);
-                    if ((lane & 3) == 0 && t + 8 * hh < w.N)
-                        r.dot[(((size_t)slab * w.B + b) * w.H + h) * w.N + t + 8 * hh] = r.sign * s;
+                    const float s = dot(m, hh);
+                    if (!strong) put_dot(m, hh, s);
                 }
             }
+            const int t = t0 + row0 + (lane >> 2);
             write_rows<T>(out + (size_t)t * row, row, acc[m], t, w.N, lane);
         }
         if (i + 1 < n || r.state_end) update<T, D>(S, kt, v, rev, wt, decay, lane);

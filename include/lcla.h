@@ -425,7 +425,12 @@ LCLA_API int lcla_gated_step(const void *q, const void *k, const void *v, const 
  *   dstate_in = e^{g_0} R_0.
  *   dq, dk, dv    [B, N, H, d] device, dtype.  dg [B, N, H] float32 device.
  *   dstate_in     [B, H, d, d] float32 device, or NULL; may be dstate_out.
- * Same rules as the forward; sums run in a fixed order.
+ * Same rules as the forward; sums run in a fixed order.  dg_t is computed as a
+ * sum over the pairs of tokens (s < t <= u) that its gate lies between, within
+ * 2^-17 of their magnitudes and exactly 0 where e^{g_t} is 0 in fp32.  Where
+ * tiles of 32 tokens keep e^-3 or more of a state it also has roundings, 2^-22
+ * of the terms <q, dq> and <k, dk>, of later tokens; and a single gate below
+ * -3 among gates near 0 has its neighbours', 2^-22 e^{-g_t} of itself.
  */
 LCLA_API size_t lcla_gated_backward_workspace_bytes(int B, int H, int N, int d, int dtype);
 LCLA_API int lcla_gated_backward(const void *dout, const void *q, const void *k, const void *v,
