@@ -296,15 +296,16 @@ LCLA_API int lcla_step(const void *q_blk, const void *k_blk, const void *v_blk,
  *   positions     [axes][N] int64 device, 8-byte aligned, or NULL: token n then
  *                 stands at index first + n of a row-major grid, pos_a =
  *                 (index / product of the extents after a) mod extent of a
- *                 (the first axis is not wrapped).  Angles are reduced exactly,
- *                 so far positions lose nothing; each entry is within 2e-7 of
- *                 amp times its cosine or sine.
+ *                 (the first axis is not wrapped).  For positions up to 2^36,
+ *                 of either sign, each entry is within 2e-7 of amp times its
+ *                 cosine or sine; beyond, a given position's angle is off by
+ *                 up to |position| 2^-64 of a turn.
  *   axis_dims     HOST array of `axes` (1..3) even sizes, sum <= 256.
  *   axis_extents  HOST array of axes - 1 extents of the inner axes (e.g. rows
  *                 and columns of a latent frame); NULL when axes = 1 or
  *                 positions are given.
  *   theta >= 1; factor >= 1 (read unless LCLA_ROPE_NONE); original_len > 0 and
- *   beta_fast > beta_slow >= 0 (read for LCLA_ROPE_YARN); 0 <= first <= 2^60.
+ *   beta_fast > beta_slow >= 0 (read for LCLA_ROPE_YARN); 0 <= first <= 2^36 - N.
  *   rope_cos/sin  [N, P] float32 device.  Written.
  * Returns an lcla_status (N = 0: LCLA_OK, nothing enqueued).
  */

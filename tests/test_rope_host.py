@@ -118,3 +118,10 @@ def test_binding_refuses():
         lcla.rotary_tables(4, 32, scaling="other")
     with pytest.raises(ValueError):
         lcla.rotary_tables(-1, 32)
+
+
+@pytest.mark.parametrize("first,code", [((1 << 36) - 100, INVALID), ((1 << 36) - 99, UNSUPPORTED), (1 << 50, UNSUPPORTED),
+                                        ((1 << 63) - 1, UNSUPPORTED)])
+def test_indices_beyond_the_angles_are_refused(first, code):
+    """The last grid index is 2^36 - 1, where an angle is still exact enough; the invalid call is refused for its NULL."""
+    assert tables(first=first, c=None) == code
