@@ -82,17 +82,34 @@ struct Shape {
     static constexpr int TOTAL_STAGES = 3;
 };
 
+// The block's recurrences, of ROLES side by side.
+template <typename T, int D, Direction DIR, bool DOT, int STAGES, int ROLES, bool CAREFUL>
+__device__ __forceinline__ bool run_block(const Work &w, const Role *roles)
+{
+    using S = Smem<T, D, DOT ? 4 : 3, STAGES>;
+    const Place p = place<D>(w.H, ROLES);
+    return p.live && recur<T, D, DIR, DOT, STAGES, CAREFUL>(w, roles[p.role], p.b, p.h, p.seg, p.group, p.slab, p.lane,
+                                                            ring_of<S>(p), weights_of<S>());
+}
+// Once more, where a value was not finite.  Not inlined, so that the first run has the registers to itself.
+template <typename T, int D, Direction DIR, bool DOT, int STAGES, int ROLES>
+__device__ __noinline__ void run_again(const Work &w, const Role *roles)
+{
+    run_block<T, D, DIR, DOT, STAGES, ROLES, true>(w, roles);
+}
+template <typename T, int D, Direction DIR, bool DOT, int STAGES, int ROLES>
+__device__ __forceinline__ void run(const Work &w, const Role *roles)
+{
+    if (run_block<T, D, DIR, DOT, STAGES, ROLES, false>(w, roles)) run_again<T, D, DIR, DOT, STAGES, ROLES>(w, roles);
+}
+
 // Bound by matrix instructions and issue slots together (100 mma.sync, about 7 cycles each beside other work, and some
 // 700 other instructions per tile and head at d = 32): 480p (70 heads, 32760 tokens, 587 MB) 128 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
 gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
 {
-    constexpr int ST = Shape<T, D>::STAGES;
-    using S = Smem<T, D, 3, ST>;
-    const Place p = place<D>(w.H, 1);
-    if (!p.live) return;
-    recur<T, D, FORWARD, false, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p), weights_of<S>());
+    run<T, D, FORWARD, false, Shape<T, D>::STAGES, 1>(w, &r);
 }
 
 // dq and dk side by side: the same instructions for both directions, since two unrolled bodies together overflow the
@@ -107,23 +124,14 @@ template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
 gated_backward_qk_k(const __grid_constant__ Work w, const __grid_constant__ Roles rs)
 {
-    constexpr int ST = Shape<T, D>::QK_STAGES;
-    using S = Smem<T, D, 4, ST>;
-    const Place p = place<D>(w.H, 2);
-    if (!p.live) return;
-    recur<T, D, EITHER, true, ST>(w, rs.r[p.role], p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p),
-                                  weights_of<S>());
+    run<T, D, EITHER, true, Shape<T, D>::QK_STAGES, 2>(w, rs.r);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
 gated_backward_v_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
 {
-    constexpr int ST = Shape<T, D>::STAGES;
-    using S = Smem<T, D, 3, ST>;
-    const Place p = place<D>(w.H, 1);
-    if (!p.live) return;
-    recur<T, D, REVERSED, false, ST>(w, r, p.b, p.h, p.seg, p.group, p.slab, p.lane, ring_of<S>(p), weights_of<S>());
+    run<T, D, REVERSED, false, Shape<T, D>::STAGES, 1>(w, &r);
 }
 
 // What each segment adds to the state (forward: k, v; gradient: also q, do reversed).  Bound as the forward, by 48
@@ -447,7 +455,11 @@ __global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__
     for (int k = 0; k < kGateTiles; ++k)
         if (k < n) {
             const float m = most[k];
-            const double X = m < 0.f ? after : fmin(fmax(after - down[k], -(double)m), (double)m);
+            double X = after;
+            if (!(m < 0.f)) {
+                X = m == 0.f ? 0.0 : after - down[k];
+                X = X > m ? m : X < -m ? -m : X;           // a NaN stays one
+            }
             const int t = (end - k) * TILE + lane;
             if (k % WARPS == warp && t < w.N)
                 p.dg[((size_t)b * w.N + t) * w.H + h] = t == 0 && !p.carried ? 0.f : (float)(X + own[k / WARPS]);

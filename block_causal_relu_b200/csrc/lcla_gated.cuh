@@ -244,6 +244,13 @@ __device__ __forceinline__ float2 lds2(uint32_t addr)
     asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
     return r;
 }
+__device__ __forceinline__ void lds4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
+{
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t lds_u(uint32_t addr)
 {
     uint32_t r;
@@ -402,6 +409,18 @@ __device__ __forceinline__ void group_sync(int group)
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * NS) : "memory");
 }
 
+template <int NS>
+__device__ __forceinline__ bool group_any(int group, bool x)
+{
+    if (NS == 1) return __any_sync(0xffffffffu, x);
+    int any;
+    asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, %3, p; selp.s32 %0, 1, 0, q;}"
+                 : "=r"(any)
+                 : "r"((unsigned)x), "r"(1 + group), "n"(32 * NS)
+                 : "memory");
+    return any != 0;
+}
+
 // The warps of a head copy 32 token rows of it into a tile; rows past N are filled with zeros.  `p` is the thread's own
 // first 16 bytes of the tile, `live` the rows before N.
 template <typename T, int D>
@@ -444,6 +463,80 @@ __device__ __forceinline__ void load_values(Values<T> &v, uint32_t vt, bool flip
     for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
         for (int m = 0; m < 2; ++m) load_t<D>(v[sb][m], vt, flip ? 1 - sb : sb, 2 * slab + m, lane);
+}
+
+// A masked score is a zero that still meets its value in the matrix units, and 0 times a NaN or an infinity would reach
+// the outputs of tokens that do not see that value.  not_finite: whether the warp's 32 values of a tile hold one (0 times
+// it is a NaN).  take_out: such values become zeros in the tile; returns the first token of each (lane: entry), in the
+// recurrence's direction.  put_back: the outputs of the tokens from there on, and the value's row of the state, become NaNs.
+template <typename T, int D>
+__device__ __forceinline__ bool not_finite(uint32_t vt, int slab, int lane)
+{
+    constexpr int PIECES = 32 * (int)sizeof(T) / 16;      // of a row's 32 values
+    uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int at = 32 * i + lane;
+        uint32_t u[4];
+        lds4(vt + Tile<T, D>::at(at / PIECES, slab * PIECES + at % PIECES), u[0], u[1], u[2], u[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (sizeof(T) == 2) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z[j]) : "r"(u[j]), "r"(0u));
+            else z[j] = __float_as_uint(fmaf(__uint_as_float(u[j]), 0.f, __uint_as_float(z[j])));
+        }
+    }
+    const uint32_t any = (z[0] | z[1]) | (z[2] | z[3]);
+    return __any_sync(0xffffffffu, (any & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) != 0);
+}
+template <typename T, int D>
+__device__ __forceinline__ int take_out(uint32_t vt, bool rev, int slab, int lane)
+{
+    int first = rev ? -1 : TILE;
+    for (int i = 0; i < TILE; ++i) {
+        const int row = rev ? i : TILE - 1 - i, byte = (32 * slab + lane) * (int)sizeof(T);
+        const uint32_t at = vt + Tile<T, D>::at(row, byte >> 4) + (byte & 15);
+        if (sizeof(T) == 4) {
+            if (!isfinite(lds(at))) {
+                first = row;
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
+            }
+        } else {
+            uint16_t u;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
+            if ((u & 0x7f80u) == 0x7f80u) {
+                first = row;
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)0) : "memory");
+            }
+        }
+    }
+    __syncwarp();
+    return first;
+}
+__device__ __forceinline__ void put_nan(float *p) { *p = __uint_as_float(0x7fffffffu); }
+__device__ __forceinline__ void put_nan(__nv_bfloat16 *p) { *reinterpret_cast<unsigned short *>(p) = 0x7fff; }
+// `out`: the warp's 32 entries of the tile's first token; dot: its first token's, or NULL.
+template <typename T, int D>
+__device__ __forceinline__ void put_back(float (&S)[2][D / 8][4], T *out, size_t row, float *dot, int first, int live,
+                                         bool rev, int lane)
+{
+    __syncwarp();                              // after the other lanes' writes to the same places
+    const int from = rev ? 0 : first, to = min(rev ? first + 1 : TILE, live);
+    for (int t = from; t < to; ++t) put_nan(out + t * row + lane);
+    if (dot && (rev ? lane <= (int)__reduce_max_sync(0xffffffffu, first) : lane >= (int)__reduce_min_sync(0xffffffffu, first)) &&
+        lane < live)
+        put_nan(dot + lane);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int f = __shfl_sync(0xffffffffu, first, 16 * m + 8 * h + (lane >> 2));
+            if (f >= 0 && f < TILE)
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) {
+                    put_nan(&S[m][e][2 * h]);
+                    put_nan(&S[m][e][2 * h + 1]);
+                }
+        }
 }
 
 // S <- decay S + sum over the tile's tokens of (weight v) k^T, for the warp's 32 values and all keys.  Each tile's
@@ -571,16 +664,18 @@ __device__ __forceinline__ void write_rows<__nv_bfloat16>(__nv_bfloat16 *out, si
 
 enum Direction { FORWARD, REVERSED, EITHER };   // EITHER: the role says which, so that both run the same instructions
 
-// One recurrence over one segment of one head.
-template <typename T, int D, Direction DIR, bool DOT, int STAGES>
-__device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h, int seg, int group, int slab, int lane,
+// One recurrence over one segment of one head.  A value that is not finite leaves the state so to the segment's end: there
+// it is looked for, and where it is found (true) the segment has to run once more with CAREFUL, which takes such values
+// out of their tiles.  (Looking in each tile cost 2 to 9 %.)
+template <typename T, int D, Direction DIR, bool DOT, int STAGES, bool CAREFUL>
+__device__ __forceinline__ bool recur(const Work &w, const Role &r, int b, int h, int seg, int group, int slab, int lane,
                                       uint32_t ring, Weights *wt)
 {
     using L = Tile<T, D>;
     constexpr int NS = D / 32, TENSORS = DOT ? 4 : 3, STAGE = TENSORS * L::BYTES;
     const int tiles = (w.N + TILE - 1) / TILE;
     const int first = seg * w.seg_tiles, n = min(w.seg_tiles, tiles - first);
-    if (n <= 0) return;
+    if (n <= 0) return false;
     const bool rev = DIR == EITHER ? r.rev : DIR == REVERSED;
     const size_t row = (size_t)w.H * D, row_bytes = row * sizeof(T);
     const size_t at = (size_t)b * w.N * row + (size_t)h * D;
@@ -630,6 +725,8 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
         load(i + STAGES - 1);
         const uint32_t qt = ring + (i % STAGES) * STAGE, kt = qt + L::BYTES, vt = kt + L::BYTES, xt = vt + L::BYTES;
         const int t0 = tile_at(i);
+        const bool bad = CAREFUL && not_finite<T, D>(vt, slab, lane);
+        const int nan_from = bad ? take_out<T, D>(vt, rev, slab, lane) : 0;
 
         // Query rows are taken 16 at a time, the block that sees one key block (itself) first: acc[m] holds the rows
         // from 16 block(m) on.
@@ -786,10 +883,27 @@ __device__ __forceinline__ void recur(const Work &w, const Role &r, int b, int h
             const int t = t0 + row0 + (lane >> 2);
             write_rows<T>(out + (size_t)t * row, row, acc[m], t, w.N, lane);
         }
+        if (bad)
+            put_back<T, D>(S, out + (size_t)t0 * row, row,
+                           DOT && !strong ? r.dot + (((size_t)slab * w.B + b) * w.H + h) * w.N + t0 : nullptr, nan_from,
+                           w.N - t0, rev, lane);
         if (i + 1 < n || r.state_end) update<T, D>(S, kt, v, rev, wt, decay, lane);
     }
     wait_copies<0>();
+    if (!CAREFUL) {
+        float2 z = both(0.f);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) z = fma2(make_float2(S[m][e][j], S[m][e][j + 1]), both(0.f), z);
+        bool bad = ((__float_as_uint(z.x) | __float_as_uint(z.y)) & 0x7fffffffu) != 0;
+        if (!r.state_end) bad |= not_finite<T, D>(ring + ((n - 1) % STAGES) * STAGE + 2 * L::BYTES, slab, lane);
+        if (group_any<NS>(group, bad)) return true;
+    }
     if (r.state_end) write_state<D>(S, r.state_end + ((size_t)b * w.H + h) * D * D, slab, lane);
+    return false;
 }
 
 // What a segment adds to the state, from zero, and its decay.  The tiles are taken against the recurrence's direction,

@@ -391,9 +391,9 @@ LCLA_API int lcla_qk_norm_rope_backward(const void *dq_out, long long lddq_out,
  *   scale         1e-18 <= |scale| <= 1e18.
  *   workspace     lcla_gated_forward_workspace_bytes(...) bytes, 16-byte
  *                 aligned (NULL when 0); not shared with a call in flight.
- * Everything else must not overlap.  q, k, v and the states must be finite: a
- * NaN or infinity of one token can also reach the outputs of the up to 31
- * tokens before it that share its tile.  With bf16 inputs, weighted scores,
+ * Everything else must not overlap.  A NaN or an infinity in q, k, v or a state
+ * reaches the outputs and states that the formulas take it to and no others
+ * (there as a NaN or an infinity).  With bf16 inputs, weighted scores,
  * weighted values and states enter the matrix units as three bf16 terms (all 24
  * bits), so that outputs are fp32 results rounded once.  fp32 factors enter as
  * two tf32 terms (22 bits), and the product of the two smaller terms is left
@@ -431,7 +431,8 @@ LCLA_API int lcla_gated_step(const void *q, const void *k, const void *v, const 
  * 2^-17 of their magnitudes and exactly 0 where e^{g_t} is 0 in fp32.  Where
  * tiles of 32 tokens keep e^-3 or more of a state it also has roundings, 2^-22
  * of the terms <q, dq> and <k, dk>, of later tokens; and a single gate below
- * -3 among gates near 0 has its neighbours', 2^-22 e^{-g_t} of itself.
+ * -3 among gates near 0 has its neighbours', 2^-22 e^{-g_t} of itself.  dg can
+ * also be a NaN up to 1024 tokens before a token whose k or v is not finite.
  */
 LCLA_API size_t lcla_gated_backward_workspace_bytes(int B, int H, int N, int d, int dtype);
 LCLA_API int lcla_gated_backward(const void *dout, const void *q, const void *k, const void *v,
