@@ -757,7 +757,9 @@ const char *lcla_status_string(int status)
     switch (status) {
     case LCLA_OK: return "ok";
     case LCLA_ERR_INVALID_ARG: return "invalid argument";
-    case LCLA_ERR_UNSUPPORTED: return "unsupported problem (head dim or size beyond what the call serves)";
+    case LCLA_ERR_UNSUPPORTED:
+        return "unsupported problem (head dims: 32 and 64, the norm any multiple of 8 up to 256, tables 256 in all; N <= 2^30; "
+               "the header gives each call's other limits)";
     case LCLA_ERR_MISALIGNED: return "array pointer not 16-byte aligned";
     case LCLA_ERR_WORKSPACE: return "workspace missing or too small";
     case LCLA_ERR_CUDA: return "CUDA launch failed";

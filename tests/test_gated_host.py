@@ -89,3 +89,8 @@ def test_binding_refuses():
         lcla.gated_forward(x, x, x, g)
     with pytest.raises(TypeError):
         lcla.gated_step(x, x, x, g, None, True)
+
+
+def test_the_unsupported_string_says_what_is_served():
+    text = lcla.lib.lcla_status_string(UNSUPPORTED).decode()
+    assert "32 and 64" in text and "256" in text and "2^30" in text
