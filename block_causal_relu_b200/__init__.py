@@ -118,6 +118,20 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _workspace(workspace: Optional[torch.Tensor], need: int, device):
+    """(workspace, its bytes): the given one, or one made of ``need`` bytes."""
+    if workspace is None:
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            return workspace, need
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def _inputs(q, k, v, cos, sin):
     for name, t in (("q", q), ("k", k), ("v", v), ("cos", cos), ("sin", sin)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -229,9 +243,7 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch.T
         out = torch.empty_like(q)
     if state_out is None and want_state:
         state_out = torch.empty((B, H, d + 1, d), dtype=torch.float32, device=q.device)
-    need = forward_workspace_bytes(B, H, N, d, block_len, code)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace, size = _workspace(workspace, forward_workspace_bytes(B, H, N, d, block_len, code), q.device)
     evp = None
     if events is not None:
         if len(events) != 4:
@@ -239,9 +251,7 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch.T
         evp = (ctypes.c_void_p * 4)(*[e.cuda_event for e in events])
     _check(lib.lcla_forward_timed(_ptr(q), _ptr(k), _ptr(v), _ptr(rope_cos), _ptr(rope_sin),
                                   B, H, N, d, int(block_len), float(eps), _ptr(out),
-                                  _ptr(state_out), code, _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(),
-                                  _stream(None, q.device), evp))
+                                  _ptr(state_out), code, _ptr(workspace), size, _stream(None, q.device), evp))
     return out, state_out
 
 
@@ -265,14 +275,10 @@ def forward_blocks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: 
         out = torch.empty_like(q)
     if state_out is None and want_state:
         state_out = torch.empty((B, H, d + 1, d), dtype=torch.float32, device=q.device)
-    need = forward_blocks_workspace_bytes(B, H, N, d, nblocks, code)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace, size = _workspace(workspace, forward_blocks_workspace_bytes(B, H, N, d, nblocks, code), q.device)
     _check(lib.lcla_forward_blocks(_ptr(q), _ptr(k), _ptr(v), _ptr(rope_cos), _ptr(rope_sin),
                                    B, H, N, d, _ptr(block_offsets), nblocks, float(eps), _ptr(out),
-                                   _ptr(state_out), code, _ptr(workspace),
-                                   0 if workspace is None else workspace.numel(),
-                                   _stream(None, q.device)))
+                                   _ptr(state_out), code, _ptr(workspace), size, _stream(None, q.device)))
     return out, state_out
 
 
@@ -303,12 +309,9 @@ def shard_begin(k: torch.Tensor, v: torch.Tensor, rope_cos: torch.Tensor, rope_s
     if total_out is None:
         total_out = torch.empty((B, H, d + 1, d), dtype=torch.float32, device=k.device)
     _state_tensor("total_out", total_out, B, H, d)
-    need = shard_workspace_bytes(B, H, N, d, block_len, code)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=k.device)
+    workspace, size = _workspace(workspace, shard_workspace_bytes(B, H, N, d, block_len, code), k.device)
     _check(lib.lcla_shard_begin(_ptr(k), _ptr(v), _ptr(rope_cos), _ptr(rope_sin), B, H, N, d, int(block_len),
-                                _ptr(total_out), code, _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _stream(None, k.device)))
+                                _ptr(total_out), code, _ptr(workspace), size, _stream(None, k.device)))
     return total_out, workspace
 
 
@@ -336,10 +339,10 @@ def shard_end(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope_cos: torch
     if state_out is None and want_state:
         state_out = torch.empty((B, H, d + 1, d), dtype=torch.float32, device=q.device)
     _state_tensor("state_out", state_out, B, H, d)
+    workspace, size = _workspace(workspace, 0, q.device)
     _check(lib.lcla_shard_end(_ptr(q), _ptr(k), _ptr(v), _ptr(rope_cos), _ptr(rope_sin), B, H, N, d,
                               int(block_len), float(eps), _ptr(totals), nranks, int(rank), _ptr(state_in),
-                              _ptr(out), _ptr(state_out), code, _ptr(workspace),
-                              0 if workspace is None else workspace.numel(), _stream(None, q.device)))
+                              _ptr(out), _ptr(state_out), code, _ptr(workspace), size, _stream(None, q.device)))
     return out, state_out
 
 
@@ -375,12 +378,9 @@ def step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor,
         raise ValueError("state must be a contiguous float32 CUDA tensor [B, H, d+1, d]")
     if out is None:
         out = torch.empty_like(q)
-    need = step_workspace_bytes(B, H, L, d, code)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace, size = _workspace(workspace, step_workspace_bytes(B, H, L, d, code), q.device)
     _check(lib.lcla_step(_ptr(q), _ptr(k), _ptr(v), _ptr(cos), _ptr(sin), B, H, L, d, float(eps),
-                         _ptr(state), int(bool(save)), _ptr(out), code, _ptr(workspace),
-                         0 if workspace is None else workspace.numel(), _stream(None, q.device)))
+                         _ptr(state), int(bool(save)), _ptr(out), code, _ptr(workspace), size, _stream(None, q.device)))
     return out
 
 
@@ -618,12 +618,6 @@ def _gated_inputs(q, k, v, g, scale):
     ptrs = (_array("q", q, shape, dtype, device), _array("k", k, shape, dtype, device),
             _array("v", v, shape, dtype, device), _array("g", g, (B, N, H), torch.float32, device))
     return ptrs, (B, H, N, d, float(d ** -0.5 if scale is None else scale)), _dtype_code(q), device
-
-
-def _workspace(workspace, need: int, device):
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _gated_need(B, H, N, d, code) -> int:
