@@ -106,6 +106,13 @@ def _check(rc: int) -> None:
         raise LclaError(rc, lib.lcla_status_string(rc).decode())
 
 
+def _ints(*sizes) -> None:
+    """Sizes go to the library as C ints, which ctypes would cut to 32 bits."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            raise LclaError(2, lib.lcla_status_string(2).decode())
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return BF16
@@ -463,7 +470,8 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
                           device=device, out=out)
     dims = [int(x) for x in ([dims] if isinstance(dims, int) else dims)]
     extents = None if extents is None else [int(x) for x in extents]
-    n = int(n)
+    n, first = int(n), int(first)
+    _ints(n, *dims, *(extents or ()), first >> 32)
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
     if not 1 <= len(dims) <= 3:
@@ -492,7 +500,7 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     else:
         ptrs = [_array(name, t, shape, torch.float32, index) for name, t in zip(("cos", "sin"), out)]
     ints = ctypes.c_int * 3
-    _run(index, lib.lcla_rotary_tables, pos, int(first), n, len(dims), ints(*dims),
+    _run(index, lib.lcla_rotary_tables, pos, first, n, len(dims), ints(*dims),
          None if extents is None else ints(*extents), float(theta), ROPE_SCALING[scaling], float(factor),
          float(original_len), float(beta_fast), float(beta_slow), *ptrs, _stream(None, index))
     return out[0], out[1]
@@ -537,6 +545,7 @@ def _norm_call(q, k, cos, sin, q_weight, k_weight, positions, eps, half_layout):
     if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
         raise ValueError("rope tables must be [rows, rotary_dims / 2]")
     rows, pairs = table = cos.shape
+    _ints(B, N, H, Hk, rows)
     f32 = torch.float32
     tail = (B, N, H, Hk, d, _array("q_weight", q_weight, (d,), f32, device),
             _array("k_weight", k_weight, (d,), f32, device), eps, _array("cos", cos, table, f32, device),
@@ -615,6 +624,7 @@ def _gated_inputs(q, k, v, g, scale):
         raise TypeError("k, v and g must be CUDA tensors")
     shape, dtype, device = q.shape, q.dtype, q.get_device()
     B, N, H, d = shape
+    _ints(B, N, H)
     ptrs = (_array("q", q, shape, dtype, device), _array("k", k, shape, dtype, device),
             _array("v", v, shape, dtype, device), _array("g", g, (B, N, H), torch.float32, device))
     return ptrs, (B, H, N, d, float(d ** -0.5 if scale is None else scale)), _dtype_code(q), device

@@ -41,3 +41,28 @@ def test_workspaces_of_every_call():
         with pytest.raises(ValueError):
             call(torch.zeros(1 << 24, 2, dtype=torch.uint8, device="cuda")[:, 0])
         call(torch.empty(1 << 22, dtype=torch.float32, device="cuda"))     # bytes count, not elements
+
+
+@pytest.mark.parametrize("kw", [dict(n=(1 << 32) + 5), dict(n=1 << 31), dict(dims=[(1 << 32) + 32]), dict(first=1 << 63),
+                                dict(first=(1 << 64) + 3), dict(first=-(1 << 64)),
+                                dict(dims=[8, 8], extents=[(1 << 32) + 7])])
+def test_sizes_that_do_not_fit_the_library_are_refused(kw):
+    """ctypes passes them modulo 2^32 (2^64): a table of other positions, or of other sizes."""
+    a = dict(n=4, dims=[32])
+    a.update(kw)
+    with pytest.raises(lcla.LclaError):
+        lcla.rotary_tables(a.pop("n"), a.pop("dims"), **a)
+
+
+@pytest.mark.gpu
+def test_tensors_of_more_tokens_than_an_int_holds():
+    """2^31 + 5 rows of 8 entries (34 GB), in place: not taken for fewer of them."""
+    if torch.cuda.mem_get_info()[0] < 50e9:
+        pytest.skip("needs 50 GB")
+    q = torch.empty(1, (1 << 31) + 5, 1, 8, device="cuda", dtype=BF)
+    c, s = lcla.rotary_tables(64, 8)
+    at = torch.zeros(1, 1, dtype=torch.int64, device="cuda").expand(1, (1 << 31) + 5)
+    with pytest.raises(lcla.LclaError):
+        lcla.qk_norm_rope(q, None, c, s, positions=at, out=(q, None))
+    with pytest.raises(lcla.LclaError):
+        lcla.qk_norm_rope_backward(q, None, q, None, c, s, positions=at, out=(q, None))
