@@ -209,7 +209,7 @@ def _on_stream(fn, stream, device, /, *args, **kw):
     that stream's memory: a block that the caller's stream has freed, with work on
     it still queued there, is not written by another one.  The results are kept
     from reuse until both streams are done with them."""
-    if device is None:
+    if device is None or torch.device(device).type != "cuda":
         return fn(*args, **kw)
     index = torch.device(device).index
     index = torch.cuda.current_device() if index is None else index
@@ -490,8 +490,10 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     elif out is not None:
         index = out[0].get_device()
     else:
-        index = torch.device(device).index
-        index = torch.cuda.current_device() if index is None else index
+        where = torch.device(device)
+        if where.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, not {where}")
+        index = torch.cuda.current_device() if where.index is None else where.index
     shape = (n, sum(dims) // 2)
     if out is None:
         cos = torch.empty(shape, dtype=torch.float32, device=f"cuda:{index}")

@@ -66,3 +66,10 @@ def test_tensors_of_more_tokens_than_an_int_holds():
         lcla.qk_norm_rope(q, None, c, s, positions=at, out=(q, None))
     with pytest.raises(lcla.LclaError):
         lcla.qk_norm_rope_backward(q, None, q, None, c, s, positions=at, out=(q, None))
+
+
+def test_tables_on_the_host_are_refused():
+    """Not made on the current CUDA device instead."""
+    for kw in (dict(), dict(stream=0)):
+        with pytest.raises(ValueError):
+            lcla.rotary_tables(4, 32, device="cpu", **kw)
