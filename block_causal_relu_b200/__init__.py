@@ -6,7 +6,9 @@ the current CUDA stream) into its entry points -- the whole-sequence forward
 (uniform or explicit blocks), the streaming step, the two halves of a
 sequence-sharded forward, the Mix-FFN temporal convolution, and the gated
 linear attention operators: rotary tables, the per-head norm of q and k with the
-rotation, and the gated recurrence with its step and gradients.  Every step of
+rotation, and the gated recurrence with its step and gradients.  No call records
+anything for autograd: a result has no graph even where an input requires a
+gradient, and a gradient is a call of its own (``*_backward``).  Every step of
 the computation runs in the library's sm_100a kernels; there is no other path.
 Importing this package fails if the library has not been built
 (``python block_causal_relu_b200/build.py``).
@@ -462,7 +464,8 @@ def rotary_tables(n: int, dims, *, extents=None, first: int = 0, positions: Opti
     ``dims`` holds the rotary dims of each axis (an int for one axis).  Tokens
     stand at ``positions`` [axes, n] ([n] for one axis) int64, or at indices
     ``first`` .. ``first + n - 1`` of a row-major grid whose inner axes have
-    the sizes ``extents``.  ``scaling``: "none", "linear", "ntk" or "yarn"."""
+    the sizes ``extents``, up to index 2^36 - 1.  ``scaling``: "none", "linear",
+    "ntk" or "yarn"."""
     if stream is not None:
         return _on_stream(rotary_tables, stream, _cuda_device(positions, *(out or ())) or device, n, dims,
                           extents=extents, first=first, positions=positions, theta=theta, scaling=scaling,
@@ -580,7 +583,8 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], rope_cos: torch.Ten
     [B, N, Hk, d] (or None), with weights [d], then the rotation of the first
     2 * rope_cos.shape[1] entries by the table rows at ``positions`` [B, N]
     int64 (token n's own row without).  q and k may be column windows of one
-    projection; ``out`` = (q_out, k_out) may be (q, k) themselves."""
+    projection; ``out`` = (q_out, k_out) may be (q, k) themselves.  No graph for
+    autograd: the gradient is ``qk_norm_rope_backward``."""
     if stream is not None:
         return _on_stream(qk_norm_rope, stream, _cuda_device(q), q, k, rope_cos, rope_sin, q_weight=q_weight,
                           k_weight=k_weight, eps=eps, positions=positions, half_layout=half_layout, out=out)
@@ -653,7 +657,8 @@ def gated_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     """``lcla_gated_forward``: S_t = exp(g_t) S_{t-1} + v_t k_t^T, out_t =
     scale S_t q_t over q, k, v [B, N, H, d] with log decays g [B, N, H] fp32 and
     scale d^-1/2 unless given.  Returns (out, state after the last token
-    [B, H, d, d] fp32 or None)."""
+    [B, H, d, d] fp32 or None).  No graph for autograd: the gradient is
+    ``gated_backward``."""
     if stream is not None:
         return _on_stream(gated_forward, stream, _cuda_device(q), q, k, v, g, scale, state_in=state_in, out=out,
                           state_out=state_out, want_state=want_state, workspace=workspace)

@@ -71,8 +71,9 @@ __device__ __forceinline__ Weights *weights_of()
 }
 
 // Blocks of a kernel on an SM, which bounds its registers, and tiles in flight per head.  Measured on the forward at
-// d = 32 (bf16, 480p): 3 blocks 205 us with 2 tiles in flight and 211 with 3, 2 blocks 215, 4 blocks 219 (they spill);
-// at d = 64: 2 blocks and 3 tiles 293, 3 and 2 309, 4 and 2 375.
+// d = 32 (bf16, 480p, passes back to back): 3 blocks 224 us with 2 tiles in flight and 241 with 3, 2 blocks 252, 4 blocks
+// 268 (they spill); at d = 64: 2 blocks and 3 tiles 346, 2 tiles 343, 4 tiles 336 (the gradient 343, 342, 344), 3 blocks and
+// 2 tiles 430.
 template <typename T, int D>
 struct Shape {
     static constexpr int BLOCKS = sizeof(T) == 2 ? (D == 32 ? 3 : 2) : 2;
@@ -103,8 +104,9 @@ __device__ __forceinline__ void run(const Work &w, const Role *roles)
     if (run_block<T, D, DIR, DOT, STAGES, ROLES, false>(w, roles)) run_again<T, D, DIR, DOT, STAGES, ROLES>(w, roles);
 }
 
-// Bound by matrix instructions and issue slots together (100 mma.sync, about 7 cycles each beside other work, and some
-// 700 other instructions per tile and head at d = 32): 480p (70 heads, 32760 tokens, 587 MB) 128 us.
+// Bound by matrix instructions and issue slots together (144 mma.sync, about 7 cycles each beside other work, and some
+// 870 other instructions per tile and head at d = 32): 480p (70 heads, 32760 tokens, 587 MB) 168 us.  fp32 at d = 64: latency
+// (255 registers, with spills, and 6 tf32 products where bf16 has 1 to 3: 6 us a tile step of one block).
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, (Shape<T, D>::BLOCKS))
 gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
@@ -114,8 +116,7 @@ gated_forward_k(const __grid_constant__ Work w, const __grid_constant__ Role r)
 
 // dq and dk side by side: the same instructions for both directions, since two unrolled bodies together overflow the
 // instruction cache (measured at d = 64: warps waited for instructions 2.3 of 6 cycles with three bodies in a launch).
-// Bound as the forward: 2 x 4680 tokens, 35
-// heads, d = 64, bf16 169 us, dv 63 us.
+// Bound as the forward: 2 x 4680 tokens, 35 heads, d = 64, bf16 179 us, dv 83 us.
 struct Roles {
     Role r[2];
 };
@@ -340,7 +341,7 @@ __device__ __forceinline__ float tile_pairs(const GradGate &p, size_t at, size_t
 // among mild ones has the roundings of its neighbours, 2^-22 e^-g of itself).
 // gated_dgate_strong_k, a warp per tile, does what a strong one needs and leaves its part of dg in the first plane;
 // gated_dgate_k, a block per segment of a head (at most 32 tiles), takes D through the segment.  Bound by latency: 2 x 4680
-// tokens, 35 heads, d = 64, bf16, 6 % of the tiles strong, 15 and 13 us from cold caches; all of them strong 66 us more.
+// tokens, 35 heads, d = 64, bf16, 6 % of the tiles strong, 16 and 14 us from cold caches; all of them strong 65 us more.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) gated_dgate_strong_k(const __grid_constant__ GradGate p)
 {
@@ -468,7 +469,8 @@ __global__ void __launch_bounds__(THREADS) gated_dgate_k(const __grid_constant__
 }
 
 // A few tokens against the state: read once, kept in registers, written once.  One block per head; D / 4 lanes hold a
-// row of the state, four entries each.  Bound by HBM: one token of 64 streams of 35 heads at d = 64 (74 MB) 14 us.
+// row of the state, four entries each.  Bound by HBM: one token of 64 streams of 35 heads at d = 64 (74 MB) 14 us
+// from cold caches, 10 with the states in L2.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS)
 gated_short_k(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const float *__restrict__ g,
@@ -516,8 +518,9 @@ constexpr size_t kAlign = 256;
 size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Calls of a few tokens take gated_short_k, whose time grows with each of them, longer ones the tiles.  Measured in
-// microseconds, tokens by tokens / tiles: bf16, 1 stream x 8 heads, d = 32: 1 token 2.0 / 3.7, 2 2.7 / 3.7, 4 3.9 / 3.7, 8
-// 6.4 / 4.1; 64 x 35, d = 64: 1 10.6 / 23.6, 4 19.9 / 24.0, 8 33.0 / 24.6; fp32, 8 x 35, d = 64: 4 6.3 / 10.0, 8 10.2 / 10.2.
+// microseconds with the states in L2, tokens by tokens / tiles: bf16, 1 stream x 8 heads, d = 32: 1 token 2.0 / 3.9, 2 2.7 /
+// 4.1, 4 3.7 / 4.2, 5 4.1 / 4.1, 8 5.7 / 4.1; 8 x 35, d = 64: 4 5.8 / 5.8, 8 9.4 / 5.8; 64 x 35, d = 64: 1 9.7 / 25.8, 4 18.4
+// / 26.0, 6 25.6 / 26.6, 8 32.0 / 26.6; fp32, 8 x 35, d = 64: 4 5.7 / 9.6, 8 9.0 / 9.6, 12 12.5 / 9.6.
 bool is_short(int N, int dtype) { return N <= (dtype == LCLA_BF16 ? 4 : 8); }
 
 struct Plan {
@@ -548,10 +551,11 @@ double kernel_time(long long n, long long ts, const StepTime &t)
 }
 
 // How many segments: the cheapest by this estimate.  Over 15 problems of 10 to 1024 tiles, each also run with 1 to 128
-// segments, its choice was the fastest or within 2 us of it, and the estimates of those above 80 us within 6 % (bf16,
-// d = 64 gradient of 2 x 35 heads: 147 tiles in 8 segments 306 us estimated, 300 measured; 10 tiles in 4 segments 44 and
-// 44, in one 75).  A step of the totals costs half of the forward's, one of dq and dk 1.4 times; the scan and the
-// launches 6 us and more with each segment.
+// segments, its choice was the fastest or within 2.1 us of it.  Its constants are of bf16 kernels with two terms: estimates
+// above 80 us are 14 % low to 4 % high (bf16, d = 64 gradient of 2 x 35 heads: 147 tiles in 8 segments 306 us estimated, 346
+// measured; 10 tiles in 4 segments 44 and 57, in one 90 measured), and constants fitted again chose worse in one problem of
+// the 15.  A step of the totals costs half of the forward's, one of dq and dk 1.4 times; the scan and the launches 6 us and
+// more with each segment.
 Plan make_plan(int B, int H, int N, int d, int dtype, bool backward)
 {
     Plan p = {};
